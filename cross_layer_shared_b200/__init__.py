@@ -70,6 +70,14 @@ SIGNATURES = {
     "sa_osk_prefill_workspace_size": ([_I, _I, _I, _I, _I, _I, _I], _SZ),
     "sa_osk_prefill": ([_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _F, _P, _P, _P, _P, _P, _I, _P, _SZ,
                         _P], _I),
+    "sa_cache_append_q8": ([_P, _I64, _P, _I64, _I, _I64, _P, _I, _P, _P, _P, _P, _P, _P, _I, _I64, _I, _I, _P, _SZ,
+                            _P], _I),
+    "sa_cache_read_q8": ([_P, _P, _P, _P, _P, _P, _I, _I64, _I, _I, _I, _P, _I, _P, _I64, _P, _P, _I, _P, _SZ, _P],
+                         _I),
+    "sa_index_score_q8": ([_P, _P, _P, _P, _P, _P, _I, _I64, _I, _I, _I, _P, _I64, _P, _SZ, _P], _I),
+    "sa_decode_attn_q8_workspace_size": ([_I, _I, _I64, _I, _I, _I, _I, _I], _SZ),
+    "sa_decode_attn_q8": ([_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I64, _I, _I, _I, _I, _I, _F, _P, _I, _P, _SZ,
+                           _P], _I),
 }
 
 
@@ -773,3 +781,259 @@ def block_union_prefill_noalloc(idx, q_pos, Q, K, V, block: int, scale: float, k
                                                 d, k, block, float(scale), _ptr(kv_indptr), _ptr(kv_indices),
                                                 _ptr(O), code, _stream(stream)))
     return kv_indptr, kv_indices, O
+
+
+# ---------------------------------------------------------------------------
+# The decode path over caches held in 8 bits: e4m3 codes [.., d] with one fp32
+# scale for each block of Q8_BLOCK tokens and KV head (the format in sa.h).
+Q8_BLOCK = 64
+
+
+def _same_device(dev: torch.device, *tensors) -> None:
+    """The kernels run on the current device: every tensor has to be there."""
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {dev}, the current device is cuda:{torch.cuda.current_device()}"
+                         if dev.type == "cuda" else f"tensors must be on the GPU, not on {dev}")
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors are on {dev} and on {t.device}")
+
+
+def _cache_q8(codes, scales, Hkv: int, d: int, name: str) -> int:
+    """Checks one 8-bit cache; returns its token places."""
+    _dev(codes, torch.float8_e4m3fn, name)
+    _dev(scales, torch.float32, f"{name}'s scales")
+    if Hkv < 1 or d < 1 or codes.shape[-1] != d or codes.numel() % (Hkv * d * Q8_BLOCK):
+        raise ValueError(f"{name} must be [.., {d}] with a multiple of {Q8_BLOCK} token places of {Hkv} heads, not "
+                         f"{tuple(codes.shape)}")
+    n_tokens = codes.numel() // (Hkv * d)
+    if scales.numel() != n_tokens * Hkv // Q8_BLOCK:
+        raise ValueError(f"{name}'s scales must be {n_tokens * Hkv // Q8_BLOCK} values, not {scales.numel()}")
+    return n_tokens
+
+
+def _pair_q8(K8, K_scale, V8, V_scale, Hkv: int, d: int) -> int:
+    n_tokens = _cache_q8(K8, K_scale, Hkv, d, "K8")
+    if (V8 is None) != (V_scale is None):
+        raise ValueError("V8 and V_scale go together")
+    if V8 is not None and _cache_q8(V8, V_scale, Hkv, d, "V8") != n_tokens:
+        raise ValueError("K8 and V8 must have one size")
+    return n_tokens
+
+
+def _new_rows(x, name: str, dtype=None) -> int:
+    """New tokens' rows [n, Hkv, d], each row of heads contiguous; returns the rows' stride in elements."""
+    if not (x.is_cuda and x.dim() == 3 and x.dtype in (torch.bfloat16, torch.float32)):
+        raise ValueError(f"{name} must be a CUDA tensor [n, Hkv, d] of torch.bfloat16 or torch.float32")
+    n, Hkv, d = x.shape
+    if x.numel() and ((d > 1 and x.stride(2) != 1) or (Hkv > 1 and x.stride(1) != d)):
+        raise ValueError(f"each token's [Hkv, d] of {name} must be contiguous")
+    return x.stride(0) if n > 1 else Hkv * d
+
+
+def cache_append_q8(new_K, new_V, K8, K_scale, V8, V_scale, seq_off, seq_len, new_off=None,
+                    max_new: Optional[int] = None, ws=None, stream=None) -> None:
+    """Quantises new tokens' rows into 8-bit caches, in place (sa_cache_append_q8).
+
+    new_K, new_V: bf16 or fp32 [n, Hkv, d] (rows may be slices of a fused
+    projection); sequence b's rows are new_off[b] .. new_off[b+1]-1 (int64
+    [B+1]; None: one row per sequence) and land behind the tokens there:
+    seq_len already counts them.  max_new: host bound of a sequence's new
+    rows (default: n).  One tensor: new_V = V8 = V_scale = None."""
+    B = seq_len.shape[0]
+    sK = _new_rows(new_K, "new_K")
+    n, Hkv, d = new_K.shape
+    if (new_V is None) != (V8 is None):
+        raise ValueError("new_V and V8 go together")
+    sV = 0
+    if new_V is not None:
+        sV = _new_rows(new_V, "new_V")
+        if new_V.shape != new_K.shape or new_V.dtype != new_K.dtype:
+            raise ValueError("new_K and new_V must have one shape and dtype")
+    n_tokens = _pair_q8(K8, K_scale, V8, V_scale, Hkv, d)
+    _seqs(seq_off, seq_len, B)
+    if new_off is None:
+        if n != B:
+            raise ValueError(f"without new_off every sequence gets one row: new_K must have {B} rows, not {n}")
+        max_new = 1
+    else:
+        _out(new_off, (B + 1,), (torch.int64,), "new_off")
+        max_new = n if max_new is None else int(max_new)
+    _same_device(K8.device, new_K, new_V, K_scale, V8, V_scale, seq_off, seq_len, new_off, ws)
+    if ws is None:
+        ws = workspace(WS_HEADER_BYTES, K8.device)
+    _ws(ws)
+    code = SA_F32 if new_K.dtype == torch.float32 else SA_BF16
+    _check(lib().sa_cache_append_q8(_ptr(new_K), sK, _ptr(new_V), sV, code, n, _ptr(new_off), max_new, _ptr(K8),
+                                    _ptr(K_scale), _ptr(V8), _ptr(V_scale), _ptr(seq_off), _ptr(seq_len), B, n_tokens,
+                                    Hkv, d, _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def cache_read_q8(K8, K_scale, V8, V_scale, seq_off, seq_len, S_max: int, Hkv: int, idx=None, out_off=None,
+                  n_out: Optional[int] = None, out_dtype=torch.bfloat16, K=None, V=None, ws=None, stream=None):
+    """Reads an 8-bit cache back (sa_cache_read_q8): the rows of the tokens
+    idx int32 [B, k] as [B, Hkv, k, d] (-1 entries: zeros), or whole
+    sequences, packed: sequence b's [Hkv, seq_len[b], d] from row
+    out_off[b]*Hkv of [n_out*Hkv, d] (out_off int64 [B+1], the running sum of
+    seq_len; n_out its last value, or K's).  Returns (K, V), or K alone
+    without V8."""
+    B, d = seq_len.shape[0], K8.shape[-1]
+    n_tokens = _pair_q8(K8, K_scale, V8, V_scale, Hkv, d)
+    _seqs(seq_off, seq_len, B)
+    if (idx is None) == (out_off is None):
+        raise ValueError("give either idx (picked rows) or out_off (whole sequences)")
+    if V is not None and V8 is None:
+        raise ValueError("V and V8 go together")
+    if idx is not None:
+        k = idx.shape[1]
+        _out(idx, (B, k), (torch.int32,), "idx")
+        n_out, shape = 0, (B, Hkv, k, d)
+    else:
+        k = 0
+        _out(out_off, (B + 1,), (torch.int64,), "out_off")
+        if n_out is None:
+            if K is None:
+                raise ValueError("give n_out, the token rows of the packed output, or K")
+            n_out = K.numel() // (Hkv * d)
+        n_out = int(n_out)
+        shape = (n_out * Hkv, d)
+    if K is None:
+        K = torch.empty(shape, dtype=out_dtype, device=K8.device)
+    if V8 is not None and V is None:
+        V = torch.empty(shape, dtype=K.dtype, device=K8.device)
+    _out(K, shape, (torch.bfloat16, torch.float32), "K")
+    if V is not None:
+        _out(V, shape, (K.dtype,), "V")
+    _same_device(K8.device, K_scale, V8, V_scale, seq_off, seq_len, idx, out_off, K, V, ws)
+    if ws is None:
+        ws = workspace(WS_HEADER_BYTES, K8.device)
+    _ws(ws)
+    code = SA_F32 if K.dtype == torch.float32 else SA_BF16
+    _check(lib().sa_cache_read_q8(_ptr(K8), _ptr(K_scale), _ptr(V8), _ptr(V_scale), _ptr(seq_off), _ptr(seq_len), B,
+                                  n_tokens, S_max, Hkv, d, _ptr(idx), k, _ptr(out_off), n_out, _ptr(K), _ptr(V), code,
+                                  _ptr(ws), ws.numel(), _stream(stream)))
+    return K if V8 is None else (K, V)
+
+
+def index_score_q8(qI, w, KI8, KI_scale, seq_off, seq_len, S_max: int, scores=None, ld: Optional[int] = None, ws=None,
+                   stream=None) -> torch.Tensor:
+    """index_score over an 8-bit key cache (sa_index_score_q8)."""
+    B, H_I, d_I = qI.shape
+    _dev(qI, torch.bfloat16, "qI"), _out(w, (B, H_I), (torch.float32,), "w")
+    n_tokens = _cache_q8(KI8, KI_scale, 1, d_I, "KI8")
+    _seqs(seq_off, seq_len, B)
+    if scores is None:
+        ld = int(ld if ld is not None else max(S_max, 1))
+        scores = torch.empty((B, ld), dtype=torch.float32, device=qI.device)
+    else:
+        have = _rows_out(scores, B, S_max, "scores")
+        if ld is not None and int(ld) != have:
+            raise ValueError(f"ld={ld} does not match scores of {have} columns")
+        ld = have
+    _same_device(qI.device, w, KI8, KI_scale, seq_off, seq_len, scores, ws)
+    if ws is None:
+        ws = workspace(WS_HEADER_BYTES, qI.device)
+    _ws(ws)
+    _check(lib().sa_index_score_q8(_ptr(qI), _ptr(w), _ptr(KI8), _ptr(KI_scale), _ptr(seq_off), _ptr(seq_len), B,
+                                   n_tokens, S_max, H_I, d_I, _ptr(scores), ld, _ptr(ws), ws.numel(),
+                                   _stream(stream)))
+    return scores
+
+
+def decode_attn_q8_workspace_size(L_g, B, n_tokens, S_max, Hq, Hkv, d, k) -> int:
+    return int(lib().sa_decode_attn_q8_workspace_size(L_g, B, n_tokens, S_max, Hq, Hkv, d, k))
+
+
+def decode_attn_q8(Q, K8, K_scale, V8, V_scale, seq_off, seq_len, S_max: int, Hkv: int, scale: float, idx=None,
+                   out_dtype=torch.bfloat16, O=None, ws=None, stream=None) -> torch.Tensor:
+    """Decode attention over 8-bit caches (sa_decode_attn_q8): Q bf16 [L, B,
+    Hq, d] over the tokens of idx int32 [B, k] (shared by the L layers), or
+    with idx None over every token of each sequence.  Returns O [L, B, Hq, d]."""
+    L, B, Hq, d = Q.shape
+    _dev(Q, torch.bfloat16, "Q")
+    n_tokens = _pair_q8(K8, K_scale, V8, V_scale, Hkv, d)
+    if V8 is None:
+        raise ValueError("V8 is missing")
+    _seqs(seq_off, seq_len, B)
+    k = 0
+    if idx is not None:
+        k = idx.shape[1]
+        _out(idx, (B, k), (torch.int32,), "idx")
+    if O is None:
+        O = torch.empty((L, B, Hq, d), dtype=out_dtype, device=Q.device)
+    _out(O, (L, B, Hq, d), (torch.bfloat16, torch.float32), "O")
+    _same_device(Q.device, K8, K_scale, V8, V_scale, seq_off, seq_len, idx, O, ws)
+    if ws is None:
+        ws = workspace(decode_attn_q8_workspace_size(L, B, n_tokens, S_max, Hq, Hkv, d, k), Q.device)
+    _ws(ws)
+    code = SA_F32 if O.dtype == torch.float32 else SA_BF16
+    _check(lib().sa_decode_attn_q8(_ptr(Q), _ptr(K8), _ptr(K_scale), _ptr(V8), _ptr(V_scale), _ptr(seq_off),
+                                   _ptr(seq_len), _ptr(idx), L, B, n_tokens, S_max, Hq, Hkv, d, k, float(scale),
+                                   _ptr(O), code, _ptr(ws), ws.numel(), _stream(stream)))
+    return O
+
+
+def decode_step_q8_workspace_size(n_layers, B, n_tokens, S_max, Hq, Hkv, d, k) -> int:
+    """Of decode_step_q8, however its layers are grouped."""
+    return max([int(lib().sa_topk_workspace_size(B, S_max, k))] +
+               [decode_attn_q8_workspace_size(n, B, n_tokens, S_max, Hq, Hkv, d, k) for n in range(1, n_layers + 1)])
+
+
+def decode_step_q8(pattern: str, qI: Sequence, w: Sequence, KI: Sequence, K: Sequence, V: Sequence, seq_off, seq_len,
+                   S_max: int, k: int, Q, Hkv: int, scale: float, out_dtype=torch.bfloat16, O=None, idx=None,
+                   scores=None, ws=None, stream=None, new_KI: Optional[Sequence] = None,
+                   new_K: Optional[Sequence] = None, new_V: Optional[Sequence] = None):
+    """decode_step over 8-bit caches: KI, K and V list a (codes, scales) pair
+    per layer (KI's entries of S layers may be None), all of one set of
+    sequences.  An F layer scores its keys and picks the top-k tokens; it and
+    the S layers behind it attend to them, neighbours that share a cache in
+    one launch.  With new_KI ([B, 1, d_I]), new_K and new_V ([B, Hkv, d]) per
+    layer, the new token's rows are quantised into the caches first, into a
+    cache that several layers list once, from the first of them.  Returns
+    (O, idx of the last F layer)."""
+    L, B, Hq, d = Q.shape
+    n = len(pattern)
+    if not (L == n and all(len(x) == n for x in (qI, w, KI, K, V))):
+        raise ValueError("every per-layer list and Q must have one entry per pattern letter")
+    if n == 0 or pattern[0] != "F" or set(pattern) - {"F", "S"}:
+        raise ValueError("the pattern is letters F and S, the first an F")
+    if (new_K is None) != (new_V is None):
+        raise ValueError("new_K and new_V go together")
+    if any(x is not None and len(x) != n for x in (new_KI, new_K, new_V)):
+        raise ValueError("new rows must be listed per layer")
+    if O is None:
+        O = torch.empty((L, B, Hq, d), dtype=out_dtype, device=Q.device)
+    if idx is None:
+        idx = torch.empty((B, k), dtype=torch.int32, device=Q.device)
+    if scores is None:
+        scores = torch.empty((B, max(S_max, 1)), dtype=torch.float32, device=Q.device)
+    if ws is None:
+        n_tokens = K[0][0].numel() // (Hkv * d)
+        ws = workspace(decode_step_q8_workspace_size(n, B, n_tokens, S_max, Hq, Hkv, d, k), Q.device)
+    done = set()  # caches that hold the new rows
+
+    def first(cache) -> bool:
+        key = cache[0].data_ptr()
+        return not (key in done or done.add(key))
+
+    if new_KI is not None:
+        for l in range(n):
+            if pattern[l] == "F" and first(KI[l]):
+                cache_append_q8(new_KI[l], None, *KI[l], None, None, seq_off, seq_len, ws=ws, stream=stream)
+    if new_K is not None:
+        for l in range(n):
+            if first(K[l]):
+                cache_append_q8(new_K[l], new_V[l], *K[l], *V[l], seq_off, seq_len, ws=ws, stream=stream)
+    l = 0
+    while l < n:
+        if pattern[l] == "F":
+            index_score_q8(qI[l], w[l], *KI[l], seq_off, seq_len, S_max, scores=scores, ws=ws, stream=stream)
+            topk(scores, seq_len, S_max, k, idx=idx, ws=ws, stream=stream)
+        end = l + 1
+        while end < n and pattern[end] == "S" and K[end][0].data_ptr() == K[l][0].data_ptr() \
+                and V[end][0].data_ptr() == V[l][0].data_ptr():
+            end += 1
+        decode_attn_q8(Q[l:end], *K[l], *V[l], seq_off, seq_len, S_max, Hkv, scale, idx=idx, O=O[l:end], ws=ws,
+                       stream=stream)
+        l = end
+    return O, idx

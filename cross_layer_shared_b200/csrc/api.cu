@@ -20,6 +20,7 @@
 #include "indexer.cuh"
 #include "route_attn.cuh"
 #include "cp.cuh"
+#include "q8.cuh"
 #include "status.cuh"
 #include "topk.cuh"
 #include "union.cuh"
@@ -103,6 +104,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 struct TmapKey {
   const void* base;
   int rank;
+  int type;  // CUtensorMapDataType
   uint64_t dims[3], strides[2];
   uint32_t box[3];
   bool operator==(const TmapKey& o) const { return memcmp(this, &o, sizeof *this) == 0; }
@@ -116,14 +118,15 @@ constexpr int kTmapCache = 16;
 thread_local TmapEntry g_tmap_cache[kTmapCache];
 thread_local int g_tmap_next = 0;
 
-// bf16 tensor map with 128-byte swizzle; dims innermost first (elements),
-// strides in bytes for dims 1.. ; box in elements.
+// Tensor map (bf16 unless said otherwise) with 128-byte swizzle; dims
+// innermost first (elements), strides in bytes for dims 1.. ; box in elements.
 sa_status make_tmap(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
-                    const uint32_t* box) {
+                    const uint32_t* box, CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
   TmapKey key;
   memset(&key, 0, sizeof key);  // padding included: the key compares as bytes
   key.base = base;
   key.rank = rank;
+  key.type = (int)type;
   for (int i = 0; i < rank && i < 3; ++i) {
     key.dims[i] = dims[i];
     key.box[i] = box[i];
@@ -137,7 +140,7 @@ sa_status make_tmap(CUtensorMap* m, const void* base, int rank, const uint64_t* 
   auto fn = encode_fn();
   if (!fn) return fail(SA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   uint32_t estr[3] = {1, 1, 1};
-  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box,
+  CUresult r = fn(m, type, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box,
                   estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(SA_ERR_INVALID_ARG, "tensor map encoding failed (CUresult %d)", (int)r);
@@ -1252,6 +1255,194 @@ sa_status sa_osk_prefill(const int32_t* idx, const int32_t* q_pos, const void* Q
   if (e != cudaSuccess) return cuda_fail("sa_osk_prefill order", e);
   return prefill_attn(Q, K, V, q_pos, kv_indptr, kv_indices, S, Nq, Hq, Hkv, block, scale, O, out_dtype,
                       status_of(ws), order, nb, tau, steps, s, "sa_osk_prefill attention");
+}
+
+// ---------------------------------------------------------------- 8-bit cache
+namespace {
+sa_status validate_q8(const void* K8, const float* Ks, const void* V8, const float* Vs, const int64_t* seq_off,
+                      const int32_t* seq_len, int B, int64_t n_tokens, int Hkv, const char* who) {
+  if (B < 0 || B > 4096) return fail(SA_ERR_INVALID_ARG, "%s: B=%d outside [0, 4096]", who, B);
+  if (Hkv < 1 || Hkv > 1024) return fail(SA_ERR_INVALID_ARG, "%s: Hkv=%d outside [1, 1024]", who, Hkv);
+  if (n_tokens < 0 || n_tokens >= (1ll << 31) || n_tokens % sa::kQ8Block != 0)
+    return fail(SA_ERR_INVALID_ARG, "%s: n_tokens=%lld must be a multiple of %d in [0, 2^31)", who,
+                (long long)n_tokens, sa::kQ8Block);
+  if ((V8 == nullptr) != (Vs == nullptr)) return fail(SA_ERR_INVALID_ARG, "%s: V8 and V_scale go together", who);
+  if (!K8 || !Ks || !seq_off || !seq_len) return fail(SA_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  if (!aligned(K8, 16) || !aligned(V8, 16)) return fail(SA_ERR_INVALID_ARG, "%s: codes must be 16-byte aligned", who);
+  if (!aligned(Ks, 4) || !aligned(Vs, 4)) return fail(SA_ERR_INVALID_ARG, "%s: scales must be 4-byte aligned", who);
+  return SA_OK;
+}
+
+bool q8_width(int d) { return d == 64 || d == 128 || d == 192 || d == 256; }
+}  // namespace
+
+sa_status sa_cache_append_q8(const void* new_K, int64_t stride_K, const void* new_V, int64_t stride_V,
+                             sa_dtype in_dtype, int64_t n_rows, const int64_t* new_off, int max_new, void* K8,
+                             float* K_scale, void* V8, float* V_scale, const int64_t* seq_off, const int32_t* seq_len,
+                             int B, int64_t n_tokens, int Hkv, int d, void* ws, size_t ws_bytes, void* stream) {
+  const char* who = "sa_cache_append_q8";
+  if (!q8_width(d)) return fail(SA_ERR_UNSUPPORTED, "%s: d=%d not in {64, 128, 192, 256}", who, d);
+  if (in_dtype != SA_BF16 && in_dtype != SA_F32) return fail(SA_ERR_INVALID_ARG, "%s: bad in_dtype", who);
+  if (max_new < 0 || n_rows < 0) return fail(SA_ERR_INVALID_ARG, "%s: negative size", who);
+  if (!new_off && (n_rows != B || max_new != 1))
+    return fail(SA_ERR_INVALID_ARG, "%s: without new_off every sequence gets one row (n_rows = B, max_new = 1)", who);
+  if ((new_V == nullptr) != (V8 == nullptr)) return fail(SA_ERR_INVALID_ARG, "%s: new_V and V8 go together", who);
+  sa_status st = validate_q8(K8, K_scale, V8, V_scale, seq_off, seq_len, B, n_tokens, Hkv, who);
+  if (st != SA_OK) return st;
+  const int64_t piece = in_dtype == SA_BF16 ? 8 : 4;  // elements in 16 bytes
+  if (stride_K < (int64_t)Hkv * d || stride_K % piece || (new_V && (stride_V < (int64_t)Hkv * d || stride_V % piece)))
+    return fail(SA_ERR_INVALID_ARG, "%s: row strides must be at least Hkv*d and a multiple of 16 bytes", who);
+  if ((st = check_ws(ws, ws_bytes, SA_WS_HEADER_BYTES, who)) != SA_OK) return st;
+  if (B == 0 || max_new == 0 || n_rows == 0) return SA_OK;
+  if (!new_K) return fail(SA_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  if (!aligned(new_K, 16) || !aligned(new_V, 16))
+    return fail(SA_ERR_INVALID_ARG, "%s: new rows must be 16-byte aligned", who);
+  sa::Q8AppendArgs a{};
+  a.rows[0] = new_K;
+  a.rows[1] = new_V;
+  a.stride[0] = stride_K;
+  a.stride[1] = stride_V;
+  a.n_rows = n_rows;
+  a.new_off = new_off;
+  a.max_new = max_new;
+  a.cache = {{(uint8_t*)K8, (uint8_t*)V8}, {K_scale, V_scale}};
+  a.seq_off = seq_off;
+  a.seq_len = seq_len;
+  a.B = B;
+  a.Hkv = Hkv;
+  a.d = d;
+  a.n_tokens = n_tokens;
+  a.in_f32 = in_dtype == SA_F32;
+  a.status = status_of(ws);
+  const cudaError_t e = sa::launch_cache_append_q8(a, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail("sa_cache_append_q8 launch", e);
+  return SA_OK;
+}
+
+sa_status sa_cache_read_q8(const void* K8, const float* K_scale, const void* V8, const float* V_scale,
+                           const int64_t* seq_off, const int32_t* seq_len, int B, int64_t n_tokens, int S_max, int Hkv,
+                           int d, const int32_t* idx, int k, const int64_t* out_off, int64_t n_out, void* K, void* V,
+                           sa_dtype out_dtype, void* ws, size_t ws_bytes, void* stream) {
+  const char* who = "sa_cache_read_q8";
+  if (!q8_width(d)) return fail(SA_ERR_UNSUPPORTED, "%s: d=%d not in {64, 128, 192, 256}", who, d);
+  if (out_dtype != SA_BF16 && out_dtype != SA_F32) return fail(SA_ERR_INVALID_ARG, "%s: bad out_dtype", who);
+  if (S_max < 0 || k < 0 || n_out < 0) return fail(SA_ERR_INVALID_ARG, "%s: negative size", who);
+  if ((idx == nullptr) == (out_off == nullptr))
+    return fail(SA_ERR_INVALID_ARG, "%s: give either idx (picked rows) or out_off (whole sequences)", who);
+  if ((V == nullptr) != (V8 == nullptr)) return fail(SA_ERR_INVALID_ARG, "%s: V and V8 go together", who);
+  sa_status st = validate_q8(K8, K_scale, V8, V_scale, seq_off, seq_len, B, n_tokens, Hkv, who);
+  if (st != SA_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, SA_WS_HEADER_BYTES, who)) != SA_OK) return st;
+  if (B == 0 || (idx ? k == 0 : S_max == 0 || n_out == 0)) return SA_OK;
+  if (!K) return fail(SA_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  if (!aligned(K, 16) || !aligned(V, 16)) return fail(SA_ERR_INVALID_ARG, "%s: K and V must be 16-byte aligned", who);
+  sa::Q8ReadArgs a{};
+  a.cache = {{(uint8_t*)K8, (uint8_t*)V8}, {(float*)K_scale, (float*)V_scale}};
+  a.seq_off = seq_off;
+  a.seq_len = seq_len;
+  a.B = B;
+  a.Hkv = Hkv;
+  a.d = d;
+  a.S_max = S_max;
+  a.n_tokens = n_tokens;
+  a.idx = idx;
+  a.k = k;
+  a.out_off = out_off;
+  a.n_out = n_out;
+  a.out[0] = K;
+  a.out[1] = V;
+  a.out_f32 = out_dtype == SA_F32;
+  a.status = status_of(ws);
+  const cudaError_t e = sa::launch_cache_read_q8(a, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail("sa_cache_read_q8 launch", e);
+  return SA_OK;
+}
+
+sa_status sa_index_score_q8(const void* qI, const float* w, const void* KI8, const float* KI_scale,
+                            const int64_t* seq_off, const int32_t* seq_len, int B, int64_t n_tokens, int S_max,
+                            int H_I, int d_I, float* scores, int64_t ld, void* ws, size_t ws_bytes, void* stream) {
+  const char* who = "sa_index_score_q8";
+  sa_status st = validate_q8(KI8, KI_scale, nullptr, nullptr, seq_off, seq_len, B, n_tokens, 1, who);
+  if (st != SA_OK) return st;
+  if (S_max < 0) return fail(SA_ERR_INVALID_ARG, "%s: S_max=%d < 0", who, S_max);
+  if (ld < S_max) return fail(SA_ERR_INVALID_ARG, "%s: ld=%lld < S_max=%d", who, (long long)ld, S_max);
+  if ((st = validate_index(qI, w, KI8, H_I, d_I, who)) != SA_OK) return st;
+  if (!scores) return fail(SA_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  if ((st = check_ws(ws, ws_bytes, SA_WS_HEADER_BYTES, who)) != SA_OK) return st;
+  if (B == 0 || S_max == 0 || n_tokens == 0) return SA_OK;
+  CUtensorMap tm;
+  const uint64_t dims[2] = {(uint64_t)d_I, (uint64_t)n_tokens};
+  const uint64_t str[1] = {(uint64_t)d_I};
+  const uint32_t box[2] = {128, 128};
+  if ((st = make_tmap(&tm, KI8, 2, dims, str, box, CU_TENSOR_MAP_DATA_TYPE_UINT8)) != SA_OK) return st;
+  sa::Q8IndexerArgs a{reinterpret_cast<const uint16_t*>(qI), w, KI_scale, seq_off, seq_len, B, n_tokens, S_max, H_I,
+                      d_I, scores, ld, status_of(ws)};
+  const cudaError_t e = sa::launch_indexer_q8(a, tm, num_sms(), (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail("sa_index_score_q8 launch", e);
+  return SA_OK;
+}
+
+size_t sa_decode_attn_q8_workspace_size(int L_g, int B, int64_t n_tokens, int S_max, int Hq, int Hkv, int d, int k) {
+  (void)d;
+  if (L_g < 1 || B < 1 || Hkv < 1 || Hq < Hkv || k < 0 || S_max < 0 || n_tokens < 0) return SA_WS_HEADER_BYTES;
+  return SA_WS_HEADER_BYTES + sa::attn_q8_scratch_bytes(sa::plan_attn_q8(L_g * (Hq / Hkv), B, Hkv, n_tokens, S_max, k,
+                                                                         num_sms(), kSmallMaxCounters));
+}
+
+sa_status sa_decode_attn_q8(const void* Q, const void* K8, const float* K_scale, const void* V8, const float* V_scale,
+                            const int64_t* seq_off, const int32_t* seq_len, const int32_t* idx, int L_g, int B,
+                            int64_t n_tokens, int S_max, int Hq, int Hkv, int d, int k, float scale, void* O,
+                            sa_dtype out_dtype, void* ws, size_t ws_bytes, void* stream) {
+  const char* who = "sa_decode_attn_q8";
+  if (L_g < 1 || L_g > 4096 || B < 1 || Hq < 1)
+    return fail(SA_ERR_INVALID_ARG, "%s: L_g (at most 4096), B and Hq must be >= 1", who);
+  if (S_max < 0) return fail(SA_ERR_INVALID_ARG, "%s: S_max=%d < 0", who, S_max);
+  if (idx ? k < 1 : k != 0) return fail(SA_ERR_INVALID_ARG, "%s: k=%d (>= 1 with idx, 0 without)", who, k);
+  if (d != 128) return fail(SA_ERR_UNSUPPORTED, "%s: d=%d (only 128 is built)", who, d);
+  if (!V8) return fail(SA_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  sa_status st = validate_q8(K8, K_scale, V8, V_scale, seq_off, seq_len, B, n_tokens, Hkv, who);
+  if (st != SA_OK) return st;
+  if (Hq % Hkv != 0) return fail(SA_ERR_INVALID_ARG, "%s: Hq=%d not a multiple of Hkv=%d", who, Hq, Hkv);
+  if (Hq / Hkv > 128) return fail(SA_ERR_UNSUPPORTED, "%s: Hq/Hkv=%d above 128", who, Hq / Hkv);
+  if (out_dtype != SA_BF16 && out_dtype != SA_F32) return fail(SA_ERR_INVALID_ARG, "%s: bad out_dtype", who);
+  if (!Q || !O) return fail(SA_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  if (!aligned(Q, 16) || !aligned(O, 16)) return fail(SA_ERR_INVALID_ARG, "%s: Q and O must be 16-byte aligned", who);
+  if (!(scale > 0.f && scale < INFINITY)) return fail(SA_ERR_INVALID_ARG, "%s: scale must be finite and > 0", who);
+  const int R = L_g * (Hq / Hkv);
+  const sa::Q8AttnPlan p = sa::plan_attn_q8(R, B, Hkv, n_tokens, S_max, k, num_sms(), kSmallMaxCounters);
+  if ((int64_t)p.units * p.n_split >= (1ll << 31)) return fail(SA_ERR_UNSUPPORTED, "%s: too many rows", who);
+  if ((st = check_ws(ws, ws_bytes, SA_WS_HEADER_BYTES + sa::attn_q8_scratch_bytes(p), who)) != SA_OK) return st;
+  sa::Q8AttnArgs a{};
+  a.Q = reinterpret_cast<const uint16_t*>(Q);
+  a.K = reinterpret_cast<const uint8_t*>(K8);
+  a.Ks = K_scale;
+  a.V = reinterpret_cast<const uint8_t*>(V8);
+  a.Vs = V_scale;
+  a.seq_off = seq_off;
+  a.seq_len = seq_len;
+  a.idx = idx;
+  a.k = k;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.G = Hq / Hkv;
+  a.R = R;
+  a.S_max = S_max;
+  a.n_tokens = n_tokens;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.O = O;
+  a.out_f32 = out_dtype == SA_F32;
+  a.n_split = p.n_split;
+  a.chunk = p.chunk;
+  uint8_t* base = reinterpret_cast<uint8_t*>(ws);
+  a.cnt = reinterpret_cast<uint32_t*>(base + kSmallCounterOffset);
+  a.po = reinterpret_cast<float*>(base + SA_WS_HEADER_BYTES);
+  a.pml = reinterpret_cast<float2*>(base + SA_WS_HEADER_BYTES +
+                                    round_up((size_t)p.units * p.n_split * p.rows * 128 * 4, 256));
+  a.status = status_of(ws);
+  const cudaError_t e = sa::launch_attn_q8(a, p, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail("sa_decode_attn_q8 launch", e);
+  return SA_OK;
 }
 
 }  // extern "C"

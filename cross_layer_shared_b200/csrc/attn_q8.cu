@@ -1,0 +1,560 @@
+// Decode attention over the 8-bit cache (format in q8.cuh), over the tokens
+// of an index or over every token:
+//   z_t = scale * ks_t (q . ck_t),  o = sum_t softmax(z)_t vs_t cv_t
+// with ck, cv the token's codes and ks, vs its blocks' scales.
+//
+// What bounds it: 256 + 8/64 bytes per (token, KV head) for 4*128*R flops, R
+// query rows.  A decode layer has R <= 8: HBM over long contexts, latency
+// over a short index.  So the kernel is built to keep many independent copies
+// in flight, and its products run on warp-level MMA tiles (a tcgen05 tile is
+// at least 64 rows, and its TMEM and commit chain costs more than a whole
+// pass here).
+//
+//   * One CTA of 8 warps per (sequence, KV head, 128 query rows, slice of the
+//     keys), two CTAs per SM.  The warps form RGW row groups of 8*NT rows
+//     times 8/RGW key groups; a key group walks its keys 16 at a time with a
+//     ring of three stages of its own (K and V codes and scales by cp.async,
+//     two passes ahead), so key groups never wait for one another.
+//   * e4m3 codes become halves exactly (one conversion per two codes), in
+//     registers: S^T = K Q^T and O^T = V^T P^T are m16n8k16 f16 MMAs with fp32
+//     accumulators.  Queries are scaled per row by a power of two into the
+//     upper half of f16's range, which keeps all 8 bits of a bf16 element
+//     over 29 binades below the row's largest.
+//   * The dims of a k-step are permuted (the dot product does not care) so
+//     that a lane's K operands are two 16-byte pieces of a row.  V^T comes
+//     from ldmatrix.trans on pairs of codes: a lane gets two dims of two keys,
+//     one byte permute turns that into two operand registers' worth of codes.
+//   * P^T's operand layout is one movmatrix away from S^T's accumulators.  For
+//     fp32 outputs P is split into two halves (22 bits); for bf16 outputs one
+//     half (11 bits, eight times finer than the output's rounding).
+//   * The V scale vs = f 2^e (f = 1 for the powers of two an append writes)
+//     joins the logit: o sums f 2^(z + e - m_o) cv with a reference m_o over
+//     z + e of its own, l sums 2^(z - m_l).  So a key's weight is held
+//     relative to the largest contribution, however far the scales are apart.
+//   * m_o moves only when some key passes it by more than 15 (log2 units) and
+//     is then set 7 below the maximum: weights stay below 2^15 and most of
+//     f16's range is above its subnormals.  l is a float: m_l moves past 60.
+//   * Padding entries and tokens past the length have codes zero and weight
+//     zero, whatever the cache holds there.
+//   * Partial results travel normalised: (m, l, o / l).  A weighted mean of V
+//     rows cannot leave V's own range, whatever the scales.
+//   * The slices of a (b, g) leave theirs in the workspace and count
+//     themselves on a counter in its header; the last one merges them and
+//     puts the counter back to zero.  Results do not depend on which is last.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "attn_warp.cuh"
+#include "q8.cuh"
+#include "sm100.cuh"
+#include "status.cuh"
+
+namespace sa {
+namespace {
+using namespace wm;
+
+constexpr int kDq = 128;
+constexpr int kWarpsQ = 8;
+constexpr int kThreadsQ = kWarpsQ * 32;
+constexpr int kKeysQ = 16;   // keys of a pass
+constexpr int kStagesQ = 3;
+constexpr int kORow = kDq + 4;
+
+struct StageQ {
+  uint8_t k[kKeysQ * kDq];  // 16-byte piece c of row r at r*128 + ((c ^ (r & 7)) << 4)
+  uint8_t v[kKeysQ * kDq];
+  float ks[kKeysQ];
+  float vs[kKeysQ];
+};
+
+template <int NT, int RGW>
+struct SmemQ {
+  static constexpr int kRows = RGW * 8 * NT;  // query rows of the CTA
+  static constexpr int kKW = kWarpsQ / RGW;   // key groups
+  union {
+    StageQ ring[kKW][kStagesQ];
+    struct {
+      float o[kKW][kRows][kORow];  // after the loop: each key group's o
+      float f[kKW][kRows];         // .. and its weight
+    } w;
+    float2 sml[q8_max_splits(kRows)][kRows];  // the merging CTA: each slice's (m, l), then (weight, -)
+  };
+  uint4 q[RGW * NT][4][32];        // the query's B fragments: [8 rows][two k-steps][lane]
+  float rf[kRows];                 // per row: softmax scale * log2(e) / query scale
+  float2 ml[kKW][kRows];           // each key group's (m, l)
+  float2 ML[kRows];                // each row's (reference, sum of weights)
+  int64_t out_off[kRows];
+  int last;
+};
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// 8x8 matrix of halves, transposed over the warp
+__device__ __forceinline__ uint32_t transpose_half(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+__device__ __forceinline__ void cp_async4(void* dst, const void* src, uint32_t src_bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src), "r"(src_bytes)
+               : "memory");
+}
+
+// a scale >= 0 as f 2^e, 1 <= f < 2; (0, 0) for one below 2^-126
+__device__ __forceinline__ void split_scale(float s, float& f, float& e) {
+  const uint32_t u = __float_as_uint(s);
+  const int x = (int)(u >> 23 & 0xff);
+  f = x == 0 ? 0.f : __uint_as_float((u & 0x7fffffu) | 0x3f800000u);
+  e = x == 0 ? 0.f : (float)(x - 127);
+}
+
+// max over the 8 lanes that hold one query row's keys
+__device__ __forceinline__ float warp_key_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+
+template <int NT, int RGW, bool PRECISE>
+__global__ void __launch_bounds__(kThreadsQ, 2) attn_q8_kernel(const Q8AttnArgs a, const int row_tiles) {
+  using Smem = SmemQ<NT, RGW>;
+  constexpr int kRows = Smem::kRows, kKW = Smem::kKW;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int gq = lane >> 2, tq = lane & 3;
+  const int rg = warp % RGW, kw = warp / RGW;  // row group, key group
+  const int gtid = rg * 32 + lane;             // thread of the key group
+  const int slice = blockIdx.x % a.n_split;
+  const int unit = blockIdx.x / a.n_split;     // (b, g, row tile)
+  const int rt = unit % row_tiles;
+  const int g = unit / row_tiles % a.Hkv, b = unit / row_tiles / a.Hkv;
+  const int row_base = rt * kQ8RowTile;
+  pdl_trigger();
+  pdl_wait();
+  const Q8Seq s = q8_seq(a.seq_off, a.seq_len, b, a.n_tokens, a.S_max);
+  if (!s.ok && tid == 0 && slice == 0) report(a.status, kErrDevice, kKernAttnQ8, b, s.len, s.cap);
+  const int n_keys = !s.ok ? 0 : a.idx ? a.k : s.len;  // entries, or tokens
+  const int e_beg = slice * a.chunk, e_end = min(n_keys, e_beg + a.chunk);
+  // slices of this unit that have keys (at least one): the others do nothing
+  const int n_live = max(1, (n_keys + a.chunk - 1) / a.chunk);
+  if (slice >= n_live) return;
+  const int64_t row0 = s.off * a.Hkv + (int64_t)g * s.cap;
+  const int e_grp = e_beg + kw * kKeysQ;  // this group's passes: e_grp + p * kKW * 16
+  const int n_pass = e_grp < e_end ? (e_end - e_grp + kKW * kKeysQ - 1) / (kKW * kKeysQ) : 0;
+
+  // token of entry lane (< 16) of pass p, or -1; entries past the length are
+  // reported when they are used
+  auto entry = [&](int p) -> int {
+    const int e = e_grp + p * (kKW * kKeysQ) + (lane & 15);
+    if (p >= n_pass || e >= e_end) return -1;
+    return a.idx ? __ldcg(&a.idx[(int64_t)b * a.k + e]) : e;
+  };
+  // pass p's copies (t: its entries) into its stage; returns which entries are tokens
+  auto issue = [&](int t, int p) -> uint32_t {
+    if (t >= s.len) {
+      if (rg == 0 && g == 0 && rt == 0 && lane < 16)
+        report(a.status, kErrDevice, kKernAttnQ8, (int64_t)b * a.k + e_grp + p * (kKW * kKeysQ) + lane, t, s.len);
+      t = -1;
+    }
+    if (p < n_pass) {
+      StageQ& st = sm.ring[kw][p % kStagesQ];
+#pragma unroll
+      for (int i = 0; i < (kKeysQ * 8 + RGW * 32 - 1) / (RGW * 32); ++i) {
+        const int j = gtid + i * (RGW * 32);  // 16-byte piece of the 16 rows
+        const int r = j >> 3, c = j & 7;
+        if (RGW * 32 <= kKeysQ * 8 || j < kKeysQ * 8) {
+          const int tr = __shfl_sync(0xffffffffu, t, r);
+          const int64_t at = (row0 + max(tr, 0)) * kDq + c * 16;
+          const uint32_t to = r * kDq + ((c ^ (r & 7)) << 4);
+          const uint32_t bytes = tr >= 0 ? 16u : 0u;
+          cp_async16(st.k + to, a.K + at, bytes);
+          cp_async16(st.v + to, a.V + at, bytes);
+        }
+      }
+      if (rg == 0) {
+        const int64_t at = (row0 + max(t, 0)) / kQ8Block;
+        cp_async4(lane < 16 ? &st.ks[lane] : &st.vs[lane - 16], (lane < 16 ? a.Ks : a.Vs) + at, t >= 0 ? 4u : 0u);
+      }
+    }
+    cp_async_commit();
+    return __ballot_sync(0xffffffffu, t >= 0);
+  };
+  auto group_sync = [&]() {
+    if (RGW == 1)
+      __syncwarp();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(kw + 1), "n"(RGW * 32) : "memory");
+  };
+
+  int t_next = entry(0);
+  const int t_second = entry(1);
+  uint32_t seen = issue(t_next, 0);  // of the pass computed next, and of the one after it
+  t_next = entry(2);
+  uint32_t seen_after = issue(t_second, 1);
+
+  // ---- the query rows as f16 fragments ----
+  for (int r = warp; r < kRows; r += kWarpsQ) {
+    const int row = row_base + r;
+    uint2 v = make_uint2(0u, 0u);
+    int64_t off = -1;
+    if (row < a.R) {
+      const int h = g * a.G + row % a.G, l = row / a.G;
+      off = (((int64_t)l * a.B + b) * a.Hq + h) * kDq;
+      v = __ldcg(reinterpret_cast<const uint2*>(a.Q + off) + lane);  // dims 4*lane ..
+    }
+    const float x0 = bf_lo(v.x), x1 = bf_hi(v.x), x2 = bf_lo(v.y), x3 = bf_hi(v.y);
+    const float mx = fmaxf(fmaxf(fabsf(x0), fabsf(x1)), fmaxf(fabsf(x2), fabsf(x3)));
+    const uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
+    // 2^e with the largest element in [2^14, 2^15); 1 for zero or non-finite rows
+    int e = mb == 0u || mb >= 0x7f800000u ? 127 : 127 + 14 + 127 - (int)(mb >> 23);
+    e = min(e, 253);  // tiny rows: as large as a float scale goes
+    const float up = __uint_as_float((uint32_t)e << 23);
+    // dims 4*lane ..: lane tq' = lane / 8 of the fragment, k-step lane % 8
+    uint2* dst = reinterpret_cast<uint2*>(&sm.q[r >> 3][(lane & 7) >> 1][(r & 7) * 4 + (lane >> 3)]) + (lane & 1);
+    *dst = make_uint2(pack_half(x0 * up, x1 * up), pack_half(x2 * up, x3 * up));
+    if (lane == 0) {
+      sm.rf[r] = a.scale_log2 / up;
+      sm.out_off[r] = off;
+    }
+  }
+  __syncthreads();
+
+  float rf[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    rf[n][0] = sm.rf[(rg * NT + n) * 8 + 2 * tq];
+    rf[n][1] = sm.rf[(rg * NT + n) * 8 + 2 * tq + 1];
+  }
+  float m_l[NT][2], m_o[NT][2], l_run[NT][2], o[NT][8][4];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    m_l[n][0] = m_l[n][1] = m_o[n][0] = m_o[n][1] = -INFINITY;
+    l_run[n][0] = l_run[n][1] = 0.f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) o[n][c][0] = o[n][c][1] = o[n][c][2] = o[n][c][3] = 0.f;
+  }
+
+  for (int p = 0; p < n_pass; ++p) {
+    cp_async_wait<1>();
+    group_sync();  // pass p has landed; pass p - 1's stage is free
+    const bool seen0 = seen >> gq & 1, seen1 = seen >> (gq + 8) & 1;
+    seen = seen_after;
+    seen_after = issue(t_next, p + 2);
+    t_next = entry(p + 3);
+    const StageQ& st = sm.ring[kw][p % kStagesQ];
+    // ---- S^T = K Q^T: lane holds keys gq, gq + 8 at rows 2tq, 2tq + 1 ----
+    float sc[NT][2][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sc[n][0][i] = sc[n][1][i] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int at = gq * kDq + (((2 * tq + i) ^ gq) << 4);
+      const uint4 k0 = *reinterpret_cast<const uint4*>(st.k + at);
+      const uint4 k1 = *reinterpret_cast<const uint4*>(st.k + at + 8 * kDq);
+      const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint32_t f[2][4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          q8_to_half4(w0[2 * j + u], f[u][0], f[u][2]);
+          q8_to_half4(w1[2 * j + u], f[u][1], f[u][3]);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const uint4 q = sm.q[rg * NT + n][2 * i + j][lane];
+          mma_f16(sc[n][0], f[0][0], f[0][1], f[0][2], f[0][3], q.x, q.y);
+          mma_f16(sc[n][1], f[1][0], f[1][1], f[1][2], f[1][3], q.z, q.w);
+        }
+      }
+    }
+    // ---- online softmax (log2 units) ----
+    const float ks0 = st.ks[gq], ks1 = st.ks[gq + 8];
+    float f0, f1, e0, e1;  // V scales f 2^e of keys gq, gq + 8
+    split_scale(st.vs[gq], f0, e0);
+    split_scale(st.vs[gq + 8], f1, e1);
+    float z[NT][4];  // [e] key gq, [2 + e] key gq + 8, row 2tq + e
+    bool over = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        z[n][e] = seen0 ? (sc[n][0][e] + sc[n][1][e]) * (ks0 * rf[n][e]) : -INFINITY;
+        z[n][2 + e] = seen1 ? (sc[n][0][2 + e] + sc[n][1][2 + e]) * (ks1 * rf[n][e]) : -INFINITY;
+        over |= fmaxf(z[n][e] + e0, z[n][2 + e] + e1) > m_o[n][e] + 15.f;
+        over |= fmaxf(z[n][e], z[n][2 + e]) > m_l[n][e] + 60.f;
+      }
+    if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float alpha[2] = {1.f, 1.f};
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float ml = warp_key_max(fmaxf(z[n][e], z[n][2 + e]));
+          const float mo = warp_key_max(fmaxf(z[n][e] + e0, z[n][2 + e] + e1));
+          if (ml > m_l[n][e] + 60.f) {  // also when the row has no reference yet
+            l_run[n][e] *= m_l[n][e] == -INFINITY ? 0.f : ex2f(m_l[n][e] - ml);
+            m_l[n][e] = ml;
+          }
+          if (mo > m_o[n][e] + 15.f) {
+            alpha[e] = m_o[n][e] == -INFINITY ? 0.f : ex2f(m_o[n][e] - (mo - 7.f));
+            m_o[n][e] = mo - 7.f;
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          o[n][c][0] *= alpha[0];
+          o[n][c][1] *= alpha[1];
+          o[n][c][2] *= alpha[0];
+          o[n][c][3] *= alpha[1];
+        }
+      }
+    }
+    uint32_t pb[NT][PRECISE ? 2 : 1][2];  // P^T's B fragments: b0 = row gq at keys 2tq, 2tq + 1, b1 = at keys + 8
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float pw[4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l_run[n][e] += (seen0 ? ex2f(z[n][e] - m_l[n][e]) : 0.f) + (seen1 ? ex2f(z[n][2 + e] - m_l[n][e]) : 0.f);
+        pw[e] = seen0 ? ex2f(z[n][e] + e0 - m_o[n][e]) * f0 : 0.f;
+        pw[2 + e] = seen1 ? ex2f(z[n][2 + e] + e1 - m_o[n][e]) * f1 : 0.f;
+      }
+      const uint32_t h0 = pack_half(pw[0], pw[1]), h1 = pack_half(pw[2], pw[3]);
+      pb[n][0][0] = transpose_half(h0);
+      pb[n][0][1] = transpose_half(h1);
+      if (PRECISE) {
+        const float2 g0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+        const float2 g1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+        pb[n][PRECISE ? 1 : 0][0] = transpose_half(pack_half(pw[0] - g0.x, pw[1] - g0.y));
+        pb[n][PRECISE ? 1 : 0][1] = transpose_half(pack_half(pw[2] - g1.x, pw[3] - g1.y));
+      }
+    }
+    // ---- O^T += V^T P^T: 16 dims (one 16-byte piece) per product ----
+    const uint32_t vbase = smem_u32(st.v) + ((lane & 15)) * kDq;  // row of this lane's ldmatrix address
+#pragma unroll
+    for (int c2 = 0; c2 < 4; ++c2) {
+      uint32_t r0, r1, r2, r3;  // keys 0-7 / 8-15 of piece 2*c2, then of piece 2*c2 + 1
+      ldsm_x4_trans(vbase + (((2 * c2 + (lane >> 4)) ^ (lane & 7)) << 4), r0, r1, r2, r3);
+      const uint32_t rr[4] = {r0, r1, r2, r3};
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint32_t f0, f1, f2, f3;  // dims 2gq, 2gq + 1 of the piece (rows gq, gq + 8 of the operand)
+        q8_to_half4(__byte_perm(rr[2 * u], 0u, 0x3120), f0, f1);
+        q8_to_half4(__byte_perm(rr[2 * u + 1], 0u, 0x3120), f2, f3);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          mma_f16(o[n][2 * c2 + u], f0, f1, f2, f3, pb[n][0][0], pb[n][0][1]);
+          if (PRECISE) mma_f16(o[n][2 * c2 + u], f0, f1, f2, f3, pb[n][PRECISE ? 1 : 0][0], pb[n][PRECISE ? 1 : 0][1]);
+        }
+      }
+    }
+  }
+  cp_async_wait<0>();
+  // the row sums over the 8 lanes that share each row
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float v = l_run[n][e];
+      v += __shfl_xor_sync(0xffffffffu, v, 4);
+      v += __shfl_xor_sync(0xffffffffu, v, 8);
+      v += __shfl_xor_sync(0xffffffffu, v, 16);
+      l_run[n][e] = v;
+    }
+  __syncthreads();  // every group is done with its ring (w shares its space)
+  // ---- the key groups' (m, l, o / l) into the CTA's ----
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = (rg * NT + n) * 8 + 2 * tq + e;
+      const float inv = l_run[n][e] == 0.f ? 0.f : 1.f / l_run[n][e];  // a NaN sum stays one
+      // 2^(m_o - m_l) in two halves: it may pass a float's range where the result does not
+      const float half_up = m_l[n][e] == -INFINITY ? 0.f : ex2f(0.5f * (m_o[n][e] - m_l[n][e]));
+      const auto value = [&](float x) { return x * inv * half_up * half_up; };
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        *reinterpret_cast<float2*>(&sm.w.o[kw][r][16 * c + 2 * gq]) =
+            make_float2(value(o[n][c][e]), value(o[n][c][2 + e]));
+      if (gq == 0) sm.ml[kw][r] = make_float2(m_l[n][e], l_run[n][e]);
+    }
+  __syncthreads();
+  const int rows = min(kRows, a.R - row_base);
+  if (tid < rows) {
+    float M = -INFINITY, L = 0.f, f[kKW];
+#pragma unroll
+    for (int i = 0; i < kKW; ++i) M = fmaxf(M, sm.ml[i][tid].x);
+#pragma unroll
+    for (int i = 0; i < kKW; ++i) {
+      const float2 ml = sm.ml[i][tid];
+      f[i] = (ml.x == -INFINITY ? 0.f : ex2f(ml.x - M)) * ml.y;
+      L += f[i];
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+    for (int i = 0; i < kKW; ++i) sm.w.f[i][tid] = f[i] * inv;
+    sm.ML[tid] = make_float2(M, L);
+  }
+  __syncthreads();
+  auto store_out = [&](int r, int c, float4 v) {
+    const int64_t off = sm.out_off[r] + c;
+    if (a.out_f32)
+      *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.O) + off) = v;
+    else
+      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.O) + off) =
+          make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+  };
+  const int64_t part0 = (int64_t)unit * a.n_split;
+  for (int i = tid; i < rows * (kDq / 4); i += kThreadsQ) {
+    const int r = i / (kDq / 4), c = i % (kDq / 4) * 4;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < kKW; ++j) {
+      const float f = sm.w.f[j][r];
+      const float4 v = *reinterpret_cast<const float4*>(&sm.w.o[j][r][c]);
+      acc.x += f * v.x;
+      acc.y += f * v.y;
+      acc.z += f * v.z;
+      acc.w += f * v.w;
+    }
+    if (n_live == 1)
+      store_out(r, c, acc);
+    else
+      __stcg(reinterpret_cast<float4*>(a.po + ((part0 + slice) * kRows + r) * kDq + c), acc);
+  }
+  if (n_live == 1) return;
+  if (tid < rows) __stcg(&a.pml[(part0 + slice) * kRows + tid], sm.ML[tid]);
+  // ---- count this slice; the last one merges ----
+  __threadfence();
+  __syncthreads();
+  if (tid == 0) sm.last = atomicAdd(&a.cnt[unit], 1u) == (unsigned)(n_live - 1);
+  __syncthreads();
+  if (!sm.last) return;
+  __threadfence();
+  for (int i = tid; i < n_live * kRows; i += kThreadsQ)
+    if (i % kRows < rows) (&sm.sml[0][0])[i] = __ldcg(&a.pml[part0 * kRows + i]);
+  __syncthreads();
+  for (int r = warp; r < rows; r += kWarpsQ) {
+    float M = -INFINITY, L = 0.f;
+    for (int i = lane; i < n_live; i += 32) M = fmaxf(M, sm.sml[i][r].x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    for (int i = lane; i < n_live; i += 32) {
+      const float2 ml = sm.sml[i][r];
+      const float f = (ml.x == -INFINITY ? 0.f : ex2f(ml.x - M)) * ml.y;
+      sm.sml[i][r].x = f;
+      L += f;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+    if (lane == 0) sm.ML[r] = make_float2(M, L == 0.f ? 0.f : 1.f / L);
+  }
+  __syncthreads();
+  for (int i = tid; i < rows * (kDq / 4); i += kThreadsQ) {
+    const int r = i / (kDq / 4), c = i % (kDq / 4) * 4;
+    const float* src = a.po + (part0 * kRows + r) * kDq + c;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int j = 0; j < n_live; ++j) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(src + (int64_t)j * kRows * kDq));
+      const float f = sm.sml[j][r].x;
+      acc.x += f * v.x;
+      acc.y += f * v.y;
+      acc.z += f * v.z;
+      acc.w += f * v.w;
+    }
+    const float inv = sm.ML[r].y;
+    store_out(r, c, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+  }
+  if (tid == 0) a.cnt[unit] = 0;  // ready for the next launch on this workspace
+}
+
+template <int NT, int RGW>
+cudaError_t launch_nt(const Q8AttnArgs& a, const Q8AttnPlan& p, cudaStream_t stream) {
+  auto kern = a.out_f32 ? attn_q8_kernel<NT, RGW, true> : attn_q8_kernel<NT, RGW, false>;
+  const size_t smem = sizeof(SmemQ<NT, RGW>);
+  cudaError_t e = ensure_smem(kern, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.units * p.n_split));
+  cfg.blockDim = dim3(kThreadsQ);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, a, p.row_tiles);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// rows a CTA takes: 8 (one n-tile), else 16 per row group, in 1, 2, 4 or 8 row groups
+int padded_rows(int R) { return R <= 8 ? 8 : R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128; }
+
+}  // namespace
+
+Q8AttnPlan plan_attn_q8(int R, int B, int Hkv, int64_t n_tokens, int S_max, int k, int sms, int max_counters) {
+  Q8AttnPlan p;
+  p.row_tiles = (R + kQ8RowTile - 1) / kQ8RowTile;
+  p.rows = padded_rows(R);
+  p.units = B * Hkv * p.row_tiles;
+  const int64_t n = k > 0 ? k : S_max;  // keys of the longest unit
+  // keys a CTA takes per round of all its key groups
+  const int round = kKeysQ * (p.rows <= 16 ? kWarpsQ : kWarpsQ * 16 / p.rows);
+  const int64_t slots = 2ll * sms;      // CTAs the GPU holds at once
+  // Little work: one wave, at most one slice per slot.  Much work (from 2048
+  // keys per slot): about four slices per slot, so that ragged sequences and
+  // the last wave even out.
+  const int64_t keys = (k > 0 ? (int64_t)B * k : n_tokens) * Hkv * p.row_tiles;
+  const int64_t even = slots / p.units > 1 ? slots / p.units : 1;
+  int64_t chunk = keys < slots * 2048 ? (n + even - 1) / even : (keys + slots * 4 - 1) / (slots * 4);
+  if (p.units > max_counters) chunk = n;
+  const int most = q8_max_splits(p.rows);
+  const int64_t least = (n + most - 1) / most;
+  if (chunk < least) chunk = least;
+  chunk = (chunk + round - 1) / round * round;
+  if (chunk < round) chunk = round;
+  if (chunk > 0x7fffff00) chunk = 0x7fffff00;
+  p.chunk = (int)chunk;
+  p.n_split = (int)((n + chunk - 1) / chunk);
+  if (p.n_split < 1) p.n_split = 1;
+  return p;
+}
+
+size_t attn_q8_scratch_bytes(const Q8AttnPlan& p) {
+  if (p.n_split <= 1) return 0;
+  const size_t n = (size_t)p.units * p.n_split * p.rows;
+  return (n * kDq * 4 + 255) / 256 * 256 + (n * 8 + 255) / 256 * 256;
+}
+
+cudaError_t launch_attn_q8(const Q8AttnArgs& a, const Q8AttnPlan& p, cudaStream_t stream) {
+  switch (p.rows) {
+    case 8: return launch_nt<1, 1>(a, p, stream);
+    case 16: return launch_nt<2, 1>(a, p, stream);
+    case 32: return launch_nt<2, 2>(a, p, stream);
+    case 64: return launch_nt<2, 4>(a, p, stream);
+    default: return launch_nt<2, 8>(a, p, stream);
+  }
+}
+
+}  // namespace sa

@@ -1,0 +1,247 @@
+// Writing tokens into the 8-bit cache (format in q8.cuh) and reading them
+// back.  Both are one pass over their data: HBM-bound for many tokens,
+// launch-latency-bound for a decode step's single tokens.
+//
+// Append.  Sequence b's n_b new tokens go to places seq_len[b] - n_b ..
+// seq_len[b] - 1.  One CTA per (sequence, touched block of 64 tokens, head,
+// tensor): it holds the block's new rows in registers from the one time they
+// are read, reduces max|x|, picks the block's scale and stores the codes.  A
+// block that already holds tokens keeps its scale unless the new ones need a
+// larger one; then the CTA also moves the old codes to it.
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "q8.cuh"
+#include "sm100.cuh"
+#include "status.cuh"
+
+namespace sa {
+namespace {
+
+constexpr int kThreadsC = 256;
+
+// 8 elements of a row as floats; kept raw until they are used
+template <bool F32>
+struct Raw8;
+template <>
+struct Raw8<false> {
+  uint4 v;
+  __device__ __forceinline__ void load(const void* p) { v = __ldcg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void clear() { v = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ float get(int i) const {
+    const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
+    return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+  }
+};
+template <>
+struct Raw8<true> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const void* p) {
+    a = __ldcg(reinterpret_cast<const float4*>(p));
+    b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ float get(int i) const {
+    const float4& q = i < 4 ? a : b;
+    return (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w;
+  }
+};
+
+template <bool F32, int D>
+__global__ void __launch_bounds__(kThreadsC) cache_append_q8_kernel(const Q8AppendArgs a) {
+  constexpr int kPieces = D / 8;                           // 8-element pieces of a row
+  constexpr int kPer = kQ8Block * kPieces / kThreadsC;     // pieces a thread holds
+  __shared__ uint32_t warp_max[kThreadsC / 32];
+  const int tid = threadIdx.x;
+  const int b = blockIdx.z, h = blockIdx.y % a.Hkv, which = blockIdx.y / a.Hkv;
+  pdl_trigger();
+  pdl_wait();
+  const Q8Seq s = q8_seq(a.seq_off, a.seq_len, b, a.n_tokens, 0x7fffffff);
+  const int64_t src0 = a.new_off ? __ldcg(reinterpret_cast<const long long*>(a.new_off) + b) : b;
+  const int64_t src1 = a.new_off ? __ldcg(reinterpret_cast<const long long*>(a.new_off) + b + 1) : b + 1;
+  const int64_t n = src1 - src0;
+  if (!s.ok || n < 0 || n > s.len || n > a.max_new || src0 < 0 || src1 > a.n_rows) {
+    if (tid == 0 && blockIdx.x == 0 && blockIdx.y == 0)
+      report(a.status, kErrDevice, kKernCacheQ8, b, s.ok ? n : -1, s.len);
+    return;
+  }
+  const int pos0 = s.len - (int)n;
+  const int t0 = (pos0 / kQ8Block + (int)blockIdx.x) * kQ8Block;  // the block's first token
+  if (n == 0 || t0 >= s.len) return;
+  const int lo = max(pos0 - t0, 0), hi = min(s.len - t0, kQ8Block);  // new tokens [lo, hi) of the block
+  const int64_t row0 = s.off * a.Hkv + (int64_t)h * s.cap + t0;
+  float* scale_p = a.cache.scales[which] + row0 / kQ8Block;
+  uint32_t old_bits = 0;  // of the scale of the tokens already there (0: none, or not a positive scale)
+  if (lo > 0) {
+    const float old = __ldcg(scale_p);
+    if (old > 0.f && old < INFINITY) old_bits = __float_as_uint(old);
+  }
+  const uint8_t* src = reinterpret_cast<const uint8_t*>(a.rows[which]);
+  constexpr int kElem = F32 ? 4 : 2;
+  const int64_t stride = a.stride[which];
+  Raw8<F32> x[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int r = (tid + i * kThreadsC) / kPieces, p = (tid + i * kThreadsC) % kPieces;
+    if (r >= lo && r < hi)
+      x[i].load(src + ((src0 + (t0 + r - pos0)) * stride + (int64_t)h * D + p * 8) * kElem);
+    else
+      x[i].clear();
+  }
+  // max|x| over the finite values, as bits (ordered like the floats)
+  uint32_t mx = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t u = __float_as_uint(x[i].get(j)) & 0x7fffffffu;
+      mx = max(mx, u < 0x7f800000u ? u : 0u);
+    }
+  mx = __reduce_max_sync(0xffffffffu, mx);
+  if ((tid & 31) == 0) warp_max[tid >> 5] = mx;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kThreadsC / 32; ++i) mx = max(mx, warp_max[i]);
+  const uint32_t bits = max(q8_scale_bits(mx), old_bits);
+  const float inv = 1.f / __uint_as_float(bits);  // exact: a power of two
+  uint8_t* dst = a.cache.codes[which] + row0 * D;
+  const bool move = lo > 0 && bits != old_bits;  // the tokens already there go to the larger scale
+  const float ratio = move ? __uint_as_float(old_bits) * inv : 1.f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int r = (tid + i * kThreadsC) / kPieces, p = (tid + i * kThreadsC) % kPieces;
+    uint2* out = reinterpret_cast<uint2*>(dst + r * D + p * 8);
+    if (r >= lo && r < hi) {
+      *out = make_uint2(
+          q8_from_float4(x[i].get(0) * inv, x[i].get(1) * inv, x[i].get(2) * inv, x[i].get(3) * inv),
+          q8_from_float4(x[i].get(4) * inv, x[i].get(5) * inv, x[i].get(6) * inv, x[i].get(7) * inv));
+    } else if (r < lo && move) {
+      const uint2 c = *out;
+      uint32_t q[2] = {c.x, c.y};
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint32_t l, u;
+        q8_to_half4(q[j], l, u);
+        const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&l));
+        const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&u));
+        q[j] = q8_from_float4(f0.x * ratio, f0.y * ratio, f1.x * ratio, f1.y * ratio);
+      }
+      *out = make_uint2(q[0], q[1]);
+    }
+  }
+  if (tid == 0 && bits != old_bits) *scale_p = __uint_as_float(bits);
+}
+
+// ---------------------------------------------------------------- reading back
+// One CTA per (sequence, 64 tokens or index entries, head, tensor).  A thread
+// takes 8 codes at a time: 8 bytes in, 16 (bf16) or 32 (fp32) out.  A code
+// times its scale is exact in fp32; bf16 rounds it only below 2^-133.
+template <bool F32>
+__global__ void __launch_bounds__(kThreadsC) cache_read_q8_kernel(const Q8ReadArgs a) {
+  const int tid = threadIdx.x;
+  const int b = blockIdx.z, h = blockIdx.y % a.Hkv, which = blockIdx.y / a.Hkv;
+  const int e0 = blockIdx.x * kQ8Block;
+  pdl_trigger();
+  pdl_wait();
+  const Q8Seq s = q8_seq(a.seq_off, a.seq_len, b, a.n_tokens, a.S_max);
+  const bool first = tid == 0 && blockIdx.x == 0 && blockIdx.y == 0;
+  if (!s.ok && first) report(a.status, kErrDevice, kKernCacheQ8, b, s.len, s.cap);
+  const int pieces = a.d / 8;
+  const int64_t row0 = s.off * a.Hkv + (int64_t)h * s.cap;
+  int n;           // entries of this sequence
+  int64_t out0;    // its first output row for this head
+  if (a.idx) {
+    n = a.k;
+    out0 = ((int64_t)b * a.Hkv + h) * a.k;
+  } else {
+    n = s.len;
+    const int64_t o = __ldcg(reinterpret_cast<const long long*>(a.out_off) + b);
+    const int64_t o1 = __ldcg(reinterpret_cast<const long long*>(a.out_off) + b + 1);
+    if (o < 0 || o1 > a.n_out || o1 - o != s.len) {
+      if (first && s.ok) report(a.status, kErrDevice, kKernCacheQ8, b, o1 - o, s.len);
+      return;
+    }
+    out0 = o * a.Hkv + (int64_t)h * s.len;
+  }
+  const int m = min(n - e0, kQ8Block);
+  for (int i = tid; i < m * pieces; i += kThreadsC) {
+    const int e = e0 + i / pieces, p = i % pieces;
+    int t = e;
+    if (a.idx) {
+      t = __ldcg(&a.idx[(int64_t)b * a.k + e]);
+      if (t >= s.len) {
+        if (p == 0 && blockIdx.y == 0) report(a.status, kErrDevice, kKernCacheQ8, (int64_t)b * a.k + e, t, s.len);
+        t = -1;
+      }
+    }
+    float v[8] = {};
+    if (t >= 0) {
+      const int64_t row = row0 + t;
+      const uint2 c = __ldcg(reinterpret_cast<const uint2*>(a.cache.codes[which] + row * a.d + p * 8));
+      const float sc = __ldcg(a.cache.scales[which] + row / kQ8Block);
+      const uint32_t q[2] = {c.x, c.y};
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint32_t l, u;
+        q8_to_half4(q[j], l, u);
+        const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&l));
+        const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&u));
+        v[4 * j] = f0.x * sc;
+        v[4 * j + 1] = f0.y * sc;
+        v[4 * j + 2] = f1.x * sc;
+        v[4 * j + 3] = f1.y * sc;
+      }
+    }
+    const int64_t at = (out0 + e) * a.d + p * 8;
+    if (F32) {
+      float4* o = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out[which]) + at);
+      o[0] = make_float4(v[0], v[1], v[2], v[3]);
+      o[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(v[2 * j + 1]), "f"(v[2 * j]));
+      *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out[which]) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+template <typename Kernel, typename Args>
+cudaError_t launch_grid(Kernel kern, const Args& a, dim3 grid, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kThreadsC);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_append_q8(const Q8AppendArgs& a, cudaStream_t stream) {
+  // blocks a sequence's new tokens can touch: one more than full blocks when they start inside one
+  const int blocks = (a.max_new + kQ8Block - 2) / kQ8Block + 1;
+  const dim3 grid(blocks, a.Hkv * (a.cache.codes[1] ? 2 : 1), a.B);
+#define SA_APPEND_CASE(DD)                                                                     \
+  if (a.d == DD)                                                                               \
+    return a.in_f32 ? launch_grid(cache_append_q8_kernel<true, DD>, a, grid, stream)           \
+                    : launch_grid(cache_append_q8_kernel<false, DD>, a, grid, stream);
+  SA_APPEND_CASE(64) SA_APPEND_CASE(128) SA_APPEND_CASE(192) SA_APPEND_CASE(256)
+#undef SA_APPEND_CASE
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_cache_read_q8(const Q8ReadArgs& a, cudaStream_t stream) {
+  const int n = a.idx ? a.k : a.S_max;
+  const dim3 grid((n + kQ8Block - 1) / kQ8Block, a.Hkv * (a.cache.codes[1] ? 2 : 1), a.B);
+  return a.out_f32 ? launch_grid(cache_read_q8_kernel<true>, a, grid, stream)
+                   : launch_grid(cache_read_q8_kernel<false>, a, grid, stream);
+}
+
+}  // namespace sa

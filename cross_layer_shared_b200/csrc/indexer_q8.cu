@@ -1,0 +1,356 @@
+// Indexer scores over an 8-bit key cache (format in q8.cuh):
+//   score[b,t] = sum_j w[b,j] max(0, q_j . K_t) = ks_t sum_j w[b,j] max(0, q_j . c_t)
+// with c_t the token's codes and ks_t >= 0 its block's scale.
+//
+// HBM-bound: a key is d_I + 4/64 bytes in and 4 out, half of what bf16 keys
+// need, for 2 H_I d_I flops.  The codes go from HBM to the tensor cores as they
+// are: tcgen05 kind::f8f6f4 multiplies e4m3 by e4m3, so only the bf16 queries
+// have to change.  Each query row is scaled by a power of two into (224, 448]
+// and split into two e4m3 parts, hi + lo: a bf16 element has 8 significant
+// bits and each part holds 4, so the split is exact down to 2^-11 of the row's
+// largest element, and below it is off by less than 2^-17 of that element.
+// Both parts multiply the same key tile into one accumulator.
+//
+// Persistent CTAs (one per SM) walk the ragged list of (sequence, 128-key
+// tile) pairs, all of them one moving window of the cache.  Warp 0 issues TMA
+// of key tiles into a ring, warp 1 the MMAs (M = 128 keys, N = H_I padded to a
+// multiple of 16, K = 32 per instruction) into one of 4 TMEM accumulators,
+// warps 2-5 apply ReLU, weights and the key scale and store one score per
+// thread, warps 6-7 split the next sequence's queries into one of two buffers
+// while the tiles of the last one run.
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "q8.cuh"
+#include "sm100.cuh"
+#include "status.cuh"
+
+namespace sa {
+namespace {
+
+constexpr int kTile = 128;
+constexpr int kAcc = 4;
+constexpr int kThreadsI = 256;
+constexpr int kMaxStagesI = 8;
+constexpr int kSmemMaxI = 232448;
+
+// instruction descriptor, kind::f8f6f4: e4m3 A and B (both K-major), fp32 accumulate
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// shared memory: barriers | tmem slot | weights of two query buffers |
+// prefix[B+1] | (1024-aligned) two query buffers | ring
+constexpr int kBarBytes = 8 * (2 * kMaxStagesI + 2 * kAcc + 4);
+constexpr int kSlotOffset = kBarBytes;
+constexpr int kWOffset = kSlotOffset + 16;
+
+template <int NH, int NPAD>  // 128-byte halves of a key row, padded heads
+struct LayoutI {
+  static constexpr int kStageBytes = NH * kTile * 128;
+  static constexpr int kPartBytes = NH * NPAD * 128;  // one e4m3 part of a sequence's queries
+  static constexpr int kQBytes = 2 * kPartBytes;
+  static constexpr int kPrefixOffset = kWOffset + 2 * NPAD * 4;
+  static constexpr int kTmemCols = kAcc * NPAD <= 64 ? 64 : kAcc * NPAD <= 128 ? 128 : 256;
+  static int q_offset(int B) { return (kPrefixOffset + 4 * (B + 1) + 1023) / 1024 * 1024; }
+  static int stages(int B) {
+    const int n = (kSmemMaxI - 1024 - q_offset(B) - 2 * kQBytes) / kStageBytes;
+    return n > kMaxStagesI ? kMaxStagesI : n;
+  }
+  static size_t smem_bytes(int B) {
+    return 1024 + (size_t)q_offset(B) + 2 * kQBytes + (size_t)stages(B) * kStageBytes;
+  }
+};
+
+// largest b with prefix[b] <= t (prefix[0] = 0, prefix[B] > t)
+__device__ __forceinline__ int tile_sequence(const int* prefix, int B, int t) {
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (prefix[mid] <= t) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+template <int NH, int NPAD>
+__global__ void __launch_bounds__(kThreadsI, 1)
+indexer_q8_kernel(const __grid_constant__ CUtensorMap tm_ki, const Q8IndexerArgs a, int n_st, int q_off) {
+  using Lay = LayoutI<NH, NPAD>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem);
+  uint64_t* empty = full + kMaxStagesI;
+  uint64_t* tfull = empty + kMaxStagesI;
+  uint64_t* tempty = tfull + kAcc;
+  uint64_t* qfull = tempty + kAcc;
+  uint64_t* qempty = qfull + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kSlotOffset);
+  float* wq = reinterpret_cast<float*>(smem + kWOffset);  // [2][NPAD]: w times the query scale's inverse
+  int* prefix = reinterpret_cast<int*>(smem + Lay::kPrefixOffset);
+  uint8_t* qbuf = smem + q_off;
+  uint8_t* ring = qbuf + 2 * Lay::kQBytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ksteps = a.d_I / 32;
+
+  pdl_trigger();
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < n_st; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+    for (int c = 0; c < kAcc; ++c) { mbar_init(&tfull[c], 1); mbar_init(&tempty[c], 4); }
+    // a query buffer is free once its MMAs are done and the four epilogue warps hold its weights
+    for (int c = 0; c < 2; ++c) { mbar_init(&qfull[c], 2); mbar_init(&qempty[c], 5); }
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_ki);
+  } else if (warp == 1) {
+    tmem_alloc(tmem_slot, Lay::kTmemCols);
+  }
+  pdl_wait();
+  if (warp == 0) {
+    // prefix[b] = tiles of the sequences before b
+    int carry = 0;
+    for (int base = 0; base < a.B; base += 32) {
+      const int b = base + lane;
+      int n = 0;
+      if (b < a.B) {
+        const Q8Seq s = q8_seq(a.seq_off, a.seq_len, b, a.n_tokens, a.S_max);
+        if (!s.ok && blockIdx.x == 0) report(a.status, kErrDevice, kKernIndexerQ8, b, a.seq_len[b], a.S_max);
+        n = (s.len + kTile - 1) / kTile;
+      }
+      int incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      if (b < a.B) prefix[b] = carry + incl - n;
+      carry += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) prefix[a.B] = carry;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int total = prefix[a.B];
+
+  if (warp == 0) {
+    // ---------------- key tiles ----------------
+    if (lane == 0) {
+      int i = 0;
+      for (int g = blockIdx.x; g < total; g += gridDim.x, ++i) {
+        const int s = i % n_st;
+        if (!mbar_wait(&empty[s], ((i / n_st) & 1) ^ 1, kWaitLimitNs)) {
+          report(a.status, kErrTimeout, kKernIndexerQ8, blockIdx.x, 0, i);
+          break;
+        }
+        const int b = tile_sequence(prefix, a.B, g);
+        const int64_t row = a.seq_off[b] + (int64_t)(g - prefix[b]) * kTile;
+        mbar_arrive_expect_tx(&full[s], Lay::kStageBytes);
+#pragma unroll
+        for (int h = 0; h < NH; ++h)
+          tma_load_2d(ring + s * Lay::kStageBytes + h * kTile * 128, &tm_ki, &full[s], h * 128, (int)row);
+      }
+      // drain: every load issued by this thread has landed before the CTA exits
+      for (int j = i - n_st; j < i; ++j)
+        if (j >= 0) mbar_wait(&full[j % n_st], (j / n_st) & 1, kWaitLimitNs);
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer ----------------
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_e4m3(128, NPAD);
+      int i = 0, cur_b = -1, nseq = 0;
+      for (int g = blockIdx.x; g < total; g += gridDim.x, ++i) {
+        const int s = i % n_st, c = i % kAcc;
+        const int b = tile_sequence(prefix, a.B, g);
+        bool ok = true;
+        if (b != cur_b) {
+          if (nseq > 0) umma_commit(&qempty[(nseq - 1) & 1]);  // the last sequence's products
+          ok = mbar_wait(&qfull[nseq & 1], (nseq >> 1) & 1, kWaitLimitNs);
+          cur_b = b;
+          ++nseq;
+        }
+        if (!ok || !mbar_wait(&full[s], (i / n_st) & 1, kWaitLimitNs) ||
+            !mbar_wait(&tempty[c], ((i / kAcc) & 1) ^ 1, kWaitLimitNs)) {
+          report(a.status, kErrTimeout, kKernIndexerQ8, blockIdx.x, 1, i);
+          break;
+        }
+        tc_fence_after();
+        const uint32_t a_base = smem_u32(ring + s * Lay::kStageBytes);
+        const uint32_t b_base = smem_u32(qbuf + ((nseq - 1) & 1) * Lay::kQBytes);
+        const uint32_t d = tmem_base + c * NPAD;
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int k = 0; k < NH * 4; ++k) {
+            if (k >= ksteps) break;
+            const int h = k / 4, kk = k % 4;
+            const uint64_t ad = umma_desc_sw128(a_base + h * kTile * 128 + kk * 32, 16, 1024);
+            const uint64_t bd =
+                umma_desc_sw128(b_base + part * Lay::kPartBytes + h * NPAD * 128 + kk * 32, 16, 1024);
+            umma_e4m3(d, ad, bd, idesc, (part | k) != 0);
+          }
+        umma_commit(&empty[s]);
+        umma_commit(&tfull[c]);
+      }
+    }
+  } else if (warp < 6) {
+    // ---------------- epilogue: ReLU, head weights, sum, key scale ----------------
+    const int quarter = warp & 3;  // TMEM lanes this warp may read
+    const int r = quarter * 32 + lane;
+    int i = 0, cur_b = -1, nseq = 0;
+    Q8Seq seq{};
+    float wr[NPAD];
+    for (int g = blockIdx.x; g < total; g += gridDim.x, ++i) {
+      const int c = i % kAcc;
+      const int b = tile_sequence(prefix, a.B, g);
+      bool ok = true;
+      if (b != cur_b) {
+        if (lane == 0) ok = mbar_wait(&qfull[nseq & 1], (nseq >> 1) & 1, kWaitLimitNs);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        __syncwarp();
+        if (ok) {
+#pragma unroll
+          for (int j = 0; j < NPAD; ++j) wr[j] = wq[(nseq & 1) * NPAD + j];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&qempty[nseq & 1]);
+        }
+        seq = q8_seq(a.seq_off, a.seq_len, b, a.n_tokens, a.S_max);
+        cur_b = b;
+        ++nseq;
+      }
+      const int t = (g - prefix[b]) * kTile + r;
+      float ks = 0.f;
+      if (t < seq.len) ks = __ldcg(&a.scales[(seq.off + t) / kQ8Block]);
+      if (lane == 0 && ok) ok = mbar_wait(&tfull[c], (i / kAcc) & 1, kWaitLimitNs);
+      if (!__shfl_sync(0xffffffffu, ok, 0)) {
+        if (lane == 0) report(a.status, kErrTimeout, kKernIndexerQ8, blockIdx.x, 2, i);
+        break;
+      }
+      tc_fence_after();
+      uint32_t v[NPAD];
+#pragma unroll
+      for (int j = 0; j < NPAD; j += 16)
+        tmem_ld16(tmem_base + ((uint32_t)(quarter * 32) << 16) + c * NPAD + j, &v[j]);
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tempty[c]);
+      if (t < seq.len) {
+        float acc = 0.f;
+#pragma unroll
+        for (int j = 0; j < NPAD; ++j)
+          if (j < a.H_I) acc = fmaf(wr[j], fmaxf(__uint_as_float(v[j]), 0.f), acc);
+        a.scores[(int64_t)b * a.ld + t] = __fadd_rn(acc * ks, 0.f);  // canonical +0
+      }
+    }
+  } else {
+    // ---------------- queries: scale, split, swizzled K-major tiles ----------------
+    int cur_b = -1, nseq = 0;
+    for (int g = blockIdx.x; g < total; g += gridDim.x) {
+      const int b = tile_sequence(prefix, a.B, g);
+      if (b == cur_b) continue;
+      cur_b = b;
+      bool ok = true;
+      if (lane == 0) ok = mbar_wait(&qempty[nseq & 1], ((nseq >> 1) & 1) ^ 1, kWaitLimitNs);
+      if (!__shfl_sync(0xffffffffu, ok, 0)) {
+        if (lane == 0) report(a.status, kErrTimeout, kKernIndexerQ8, blockIdx.x, 3, nseq);
+        break;
+      }
+      uint8_t* hi = qbuf + (nseq & 1) * Lay::kQBytes;
+      uint8_t* lo = hi + Lay::kPartBytes;
+      for (int j = warp - 6; j < a.H_I; j += 2) {
+        const uint16_t* q = a.qI + ((int64_t)b * a.H_I + j) * a.d_I;
+        float x[NH][4];  // dims 4 * lane .. of each half
+        uint32_t mx = 0;
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          const int dim = h * 128 + lane * 4;
+          const uint2 v = dim < a.d_I ? __ldcg(reinterpret_cast<const uint2*>(q + dim)) : make_uint2(0u, 0u);
+          x[h][0] = __uint_as_float(v.x << 16);
+          x[h][1] = __uint_as_float(v.x & 0xffff0000u);
+          x[h][2] = __uint_as_float(v.y << 16);
+          x[h][3] = __uint_as_float(v.y & 0xffff0000u);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) mx = max(mx, __float_as_uint(x[h][u]) & 0x7fffffffu);
+        }
+        mx = __reduce_max_sync(0xffffffffu, mx);
+        const uint32_t sb = mx >= 0x7f800000u ? 0x3f800000u : q8_scale_bits(mx);
+        const float inv = 1.f / __uint_as_float(sb);
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          if (h * 128 + lane * 4 >= a.d_I) continue;
+          float y[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) y[u] = x[h][u] * inv;
+          const uint32_t ch = q8_from_float4(y[0], y[1], y[2], y[3]);
+          uint32_t p0, p1;
+          q8_to_half4(ch, p0, p1);
+          const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&p0));
+          const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&p1));
+          const uint32_t cl = q8_from_float4(y[0] - f0.x, y[1] - f0.y, y[2] - f1.x, y[3] - f1.y);
+          const uint32_t to = h * NPAD * 128 + sw128_offset(j, lane >> 2) + (lane & 3) * 4;
+          *reinterpret_cast<uint32_t*>(hi + to) = ch;
+          *reinterpret_cast<uint32_t*>(lo + to) = cl;
+        }
+        if (lane == 0) wq[(nseq & 1) * NPAD + j] = __ldcg(&a.w[(int64_t)b * a.H_I + j]) * __uint_as_float(sb);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&qfull[nseq & 1]);
+      ++nseq;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, Lay::kTmemCols);
+  }
+}
+
+template <int NH, int NPAD>
+cudaError_t launch_nh(const Q8IndexerArgs& a, const CUtensorMap& tm_ki, int num_sms, cudaStream_t stream) {
+  using Lay = LayoutI<NH, NPAD>;
+  auto kern = indexer_q8_kernel<NH, NPAD>;
+  if (Lay::stages(a.B) < 2) return cudaErrorInvalidValue;  // the prefix table would crowd out the ring
+  const size_t smem = Lay::smem_bytes(a.B);
+  cudaError_t e = ensure_smem(kern, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (int64_t)a.B * ((a.S_max + kTile - 1) / kTile);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles < num_sms ? tiles : num_sms));
+  cfg.blockDim = dim3(kThreadsI);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, tm_ki, a, Lay::stages(a.B), Lay::q_offset(a.B));
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_indexer_q8(const Q8IndexerArgs& a, const CUtensorMap& tm_ki, int num_sms, cudaStream_t stream) {
+  const int nh = (a.d_I + 127) / 128, npad = (a.H_I + 15) / 16 * 16;
+#define SA_IDX_CASE(NH, NP) \
+  if (nh == NH && npad == NP) return launch_nh<NH, NP>(a, tm_ki, num_sms, stream);
+  SA_IDX_CASE(1, 16) SA_IDX_CASE(1, 32) SA_IDX_CASE(1, 48) SA_IDX_CASE(1, 64)
+  SA_IDX_CASE(2, 16) SA_IDX_CASE(2, 32) SA_IDX_CASE(2, 48) SA_IDX_CASE(2, 64)
+#undef SA_IDX_CASE
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace sa

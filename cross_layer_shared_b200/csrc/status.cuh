@@ -32,6 +32,9 @@ enum : int {
   kKernRoute = 7,
   kKernWaitProbe = 8,
   kKernCp = 9,
+  kKernCacheQ8 = 10,
+  kKernIndexerQ8 = 11,
+  kKernAttnQ8 = 12,
 };
 
 struct DeviceStatus {

@@ -41,8 +41,8 @@
  *   by the matching *_workspace_size() function.  Its first
  *   SA_WS_HEADER_BYTES bytes are the header: the status block (the first
  *   256 bytes) and the slice counters of sa_sparse_decode_attn's path for
- *   few rows per KV head.  Zero the header once when the workspace is
- *   allocated: the library only ever writes a non-zero code into the status
+ *   few rows per KV head and of sa_decode_attn_q8.  Zero the header once when
+ *   the workspace is allocated: the library only ever writes a non-zero code into the status
  *   block (so the status is sticky until sa_clear_device_status(), which
  *   zeroes the whole header), and every launch leaves the counters it used
  *   at zero when it ends.  The rest is scratch owned by the call while it
@@ -581,6 +581,107 @@ sa_status sa_cp_select(const float* cand_scores, const int32_t* cand_idx, int64_
  * returns SA_OK without a launch.  No workspace. */
 sa_status sa_combine_partials(const float* O_part, int64_t o_stride, const float* ml, int64_t ml_stride,
                               int P, int64_t rows, int d, void* O, sa_dtype out_dtype, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The same decode path over caches held in 8 bits.  The pages keep their
+ * caches in the model's type; these entry points halve the bytes a decode
+ * step reads, which is what bounds it.
+ *
+ * The format.  An 8-bit cache is a tensor of e4m3 codes (1 sign, 4 exponent,
+ * 3 mantissa bits, largest value 448) and fp32 scales, one for each block of
+ * 64 tokens and KV head; a cached element is x = scale * code.  The scale is
+ * a power of two: the smallest 2^e >= 2^-126 with max|x| <= 448 * 2^e over
+ * the block's finite elements (2^-126 for a block of zeros); the code is the
+ * e4m3 value nearest to x / scale, ties to the even code.  An element
+ * carries a relative error of at most 2^-4, or 2^-17.8 of the block's
+ * largest element where that is more.  (Readers take any finite scale >= 0;
+ * one below 2^-126 counts as zero in sa_decode_attn_q8's values.)
+ *
+ *   K8, V8    e4m3 codes, n_tokens * Hkv rows of d: sequence b owns the token
+ *             places [seq_off[b], seq_off[b+1]) (its capacity, cap_b of
+ *             them) and is laid out [Hkv, cap_b, d] from row seq_off[b]*Hkv.
+ *             An indexer-key cache is the case Hkv = 1, d = d_I.
+ *   K_scale, V_scale  fp32 [n_tokens * Hkv / 64]: row r's is number r / 64
+ *   seq_off   int64 [B+1] (device), every entry a multiple of 64, <= n_tokens
+ *   seq_len   int32 [B] (device), tokens in the cache, <= cap_b
+ *   n_tokens  token places in all, a multiple of 64
+ * What lies past seq_len[b] is never used, whatever it holds.
+ * Device errors (SA_ERR_DEVICE): offsets or a length that break these rules;
+ * the sequence then counts as empty.  Every workspace is SA_WS_HEADER_BYTES
+ * unless a size function is given.
+ * ---------------------------------------------------------------------- */
+
+/* Appends new tokens, quantising them.  seq_len[b] already counts them: the
+ * n_b new tokens of sequence b go to places seq_len[b] - n_b .. seq_len[b]-1.
+ * A block that already holds tokens keeps its scale unless the new ones
+ * need a larger one; its older codes c then become the e4m3 values nearest
+ * to c * old_scale / new_scale (exact, unless they become subnormal; an old
+ * scale that is not positive and finite counts as 0).
+ * Places past seq_len[b] and all other blocks are left as they are.
+ *   new_K, new_V  bf16 or fp32 (in_dtype) [n_rows, Hkv, d], one row of heads
+ *             per token, stride_K / stride_V elements apart (so they may be
+ *             slices of a fused projection), 16-byte aligned; new_V and V8
+ *             NULL: one tensor
+ *   new_off   int64 [B+1] (device): sequence b's rows are new_off[b] ..
+ *             new_off[b+1]-1 (n_b may be 0); NULL: one row per sequence
+ *   max_new   host upper bound of n_b
+ * NaN elements get the NaN code and infinite ones the largest code of the
+ * block's scale; neither counts towards it.  Supported: d in {64, 128, 192,
+ * 256}.  Device errors: n_b outside [0, min(max_new, seq_len[b])] or rows
+ * past n_rows -> SA_ERR_DEVICE, nothing of the sequence is written. */
+sa_status sa_cache_append_q8(const void* new_K, int64_t stride_K, const void* new_V, int64_t stride_V,
+                             sa_dtype in_dtype, int64_t n_rows, const int64_t* new_off, int max_new, void* K8,
+                             float* K_scale, void* V8, float* V_scale, const int64_t* seq_off,
+                             const int32_t* seq_len, int B, int64_t n_tokens, int Hkv, int d, void* ws,
+                             size_t ws_bytes, void* stream);
+
+/* Reads cached rows back as bf16 or fp32 (out_dtype).  Either
+ *   idx int32 [B, k] (device): K, V [B, Hkv, k, d] get the picked tokens'
+ *             rows; an entry < 0 gives a row of zeros, as does one >=
+ *             seq_len[b], which is also reported (SA_ERR_DEVICE); or
+ *   out_off int64 [B+1] (device): whole sequences, sequence b's to element
+ *             out_off[b]*Hkv*d, laid out [Hkv, seq_len[b], d]: the packed bf16
+ *             cache that sa_sparse_decode_attn (with seq_off = out_off) and,
+ *             for one sequence, sa_block_union_prefill read.  out_off[b+1] -
+ *             out_off[b] must be seq_len[b] and out_off[B] <= n_out, the
+ *             token rows K and V have room for (SA_ERR_DEVICE otherwise, and
+ *             the sequence is not written).
+ * V and V8 NULL: one tensor.  S_max >= every seq_len.  Supported: d in {64,
+ * 128, 192, 256}. */
+sa_status sa_cache_read_q8(const void* K8, const float* K_scale, const void* V8, const float* V_scale,
+                           const int64_t* seq_off, const int32_t* seq_len, int B, int64_t n_tokens, int S_max,
+                           int Hkv, int d, const int32_t* idx, int k, const int64_t* out_off, int64_t n_out,
+                           void* K, void* V, sa_dtype out_dtype, void* ws, size_t ws_bytes, void* stream);
+
+/* sa_index_score over an 8-bit key cache KI8 [n_tokens, d_I] (Hkv = 1):
+ *   scores[b*ld + t] = sum_j w[b,j] * max(0, sum_c qI[b,j,c] * KI[seq_off[b]+t, c])
+ * for t in [0, seq_len[b]), fp32 accumulation, canonical +0; entries t >=
+ * seq_len[b] are left untouched.  The queries stay bf16 (finite): they enter
+ * the products as two e4m3 parts, exact but for elements below 2^-11 of their
+ * row's largest, which are off by at most 2^-17 of it.
+ * Supported: 1 <= H_I <= 64, d_I in {64, 128, 192, 256}. */
+sa_status sa_index_score_q8(const void* qI, const float* w, const void* KI8, const float* KI_scale,
+                            const int64_t* seq_off, const int32_t* seq_len, int B, int64_t n_tokens, int S_max,
+                            int H_I, int d_I, float* scores, int64_t ld, void* ws, size_t ws_bytes, void* stream);
+
+/* Decode attention over 8-bit caches, arguments and result as
+ * sa_sparse_decode_attn: for layer l < L_g, sequence b, query head h (KV head
+ * g = h / (Hq/Hkv))
+ *   z_t = scale * Q[l,b,h,:] . K_b[g,t,:],   O[l,b,h,:] = sum_t softmax(z)_t * V_b[g,t,:]
+ * over the tokens of idx[b,:] (entries < 0 skipped, a token listed twice
+ * counts twice), or with idx = NULL and k = 0 over every token t <
+ * seq_len[b] (a dense layer).  fp32 softmax and accumulation.  A row with no
+ * token gets O = 0.  S_max >= every seq_len.  Supported: d = 128, Hq % Hkv ==
+ * 0, Hq/Hkv <= 128.
+ * Device errors: idx entry >= seq_len[b] -> SA_ERR_DEVICE, entry skipped.
+ * Keys are split over several CTAs whose partial results meet in the
+ * workspace (counted in its header), whose size this gives: */
+size_t sa_decode_attn_q8_workspace_size(int L_g, int B, int64_t n_tokens, int S_max, int Hq, int Hkv, int d, int k);
+sa_status sa_decode_attn_q8(const void* Q, const void* K8, const float* K_scale, const void* V8,
+                            const float* V_scale, const int64_t* seq_off, const int32_t* seq_len,
+                            const int32_t* idx, int L_g, int B, int64_t n_tokens, int S_max, int Hq, int Hkv,
+                            int d, int k, float scale, void* O, sa_dtype out_dtype, void* ws, size_t ws_bytes,
+                            void* stream);
 
 #ifdef __cplusplus
 }
