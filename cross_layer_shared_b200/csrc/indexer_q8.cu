@@ -9,15 +9,18 @@
 // and split into two e4m3 parts, hi + lo: a bf16 element has 8 significant
 // bits and each part holds 4, so the split is exact down to 2^-11 of the row's
 // largest element, and below it is off by less than 2^-17 of that element.
-// Both parts multiply the same key tile into one accumulator.
+// Both parts are columns of one B operand, so a key tile is read from shared
+// memory once for them; the epilogue adds the two columns of a head.
 //
-// Persistent CTAs (one per SM) walk the ragged list of (sequence, 128-key
-// tile) pairs, all of them one moving window of the cache.  Warp 0 issues TMA
-// of key tiles into a ring, warp 1 the MMAs (M = 128 keys, N = H_I padded to a
-// multiple of 16, K = 32 per instruction) into one of 4 TMEM accumulators,
-// warps 2-5 apply ReLU, weights and the key scale and store one score per
-// thread, warps 6-7 split the next sequence's queries into one of two buffers
-// while the tiles of the last one run.
+// Persistent CTAs take equal contiguous ranges of the ragged list of
+// (sequence, 128-key tile) pairs, so that a CTA meets few sequences.  Warp 0
+// issues TMA of key tiles into a ring, warp 1 the MMAs (M = 128 keys, N = two
+// parts of H_I heads padded to a multiple of 8, K = 32 per instruction) into
+// one of several TMEM accumulators, warps 2-5 apply ReLU, weights and the key
+// scale and store one score per thread, warps 6-7 split the next sequence's
+// queries into one of two buffers while the tiles of the last one run.  Two
+// CTAs share an SM where each still has four stages: a tile passes TMA, MMA
+// and epilogue one after another, and a second chain fills the gaps.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -31,10 +34,11 @@ namespace sa {
 namespace {
 
 constexpr int kTile = 128;
-constexpr int kAcc = 4;
+constexpr int kMaxAcc = 4;
 constexpr int kThreadsI = 256;
 constexpr int kMaxStagesI = 8;
-constexpr int kSmemMaxI = 232448;
+constexpr int kSmemMaxI = 232448;   // of a CTA alone on its SM
+constexpr int kSmemHalfI = 115712;  // of each of two
 
 // instruction descriptor, kind::f8f6f4: e4m3 A and B (both K-major), fp32 accumulate
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
@@ -53,24 +57,26 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint
 
 // shared memory: barriers | tmem slot | weights of two query buffers |
 // prefix[B+1] | (1024-aligned) two query buffers | ring
-constexpr int kBarBytes = 8 * (2 * kMaxStagesI + 2 * kAcc + 4);
+constexpr int kBarBytes = 8 * (2 * kMaxStagesI + 2 * kMaxAcc + 4);
 constexpr int kSlotOffset = kBarBytes;
 constexpr int kWOffset = kSlotOffset + 16;
 
 template <int NH, int NPAD>  // 128-byte halves of a key row, padded heads
 struct LayoutI {
+  static constexpr int kCols = 2 * NPAD;              // of one accumulator
+  static constexpr int kAcc = kCols <= 64 ? 4 : 2;
+  static constexpr int kTmemCols = kAcc * kCols <= 64 ? 64 : kAcc * kCols <= 128 ? 128 : 256;
   static constexpr int kStageBytes = NH * kTile * 128;
-  static constexpr int kPartBytes = NH * NPAD * 128;  // one e4m3 part of a sequence's queries
-  static constexpr int kQBytes = 2 * kPartBytes;
+  static constexpr int kQHalf = kCols * 128;          // [hi heads | lo heads] x 128 bytes
+  static constexpr int kQBytes = NH * kQHalf;
   static constexpr int kPrefixOffset = kWOffset + 2 * NPAD * 4;
-  static constexpr int kTmemCols = kAcc * NPAD <= 64 ? 64 : kAcc * NPAD <= 128 ? 128 : 256;
   static int q_offset(int B) { return (kPrefixOffset + 4 * (B + 1) + 1023) / 1024 * 1024; }
-  static int stages(int B) {
-    const int n = (kSmemMaxI - 1024 - q_offset(B) - 2 * kQBytes) / kStageBytes;
+  static int stages(int B, int smem) {
+    const int n = (smem - 1024 - q_offset(B) - 2 * kQBytes) / kStageBytes;
     return n > kMaxStagesI ? kMaxStagesI : n;
   }
-  static size_t smem_bytes(int B) {
-    return 1024 + (size_t)q_offset(B) + 2 * kQBytes + (size_t)stages(B) * kStageBytes;
+  static size_t smem_bytes(int B, int n_st) {
+    return 1024 + (size_t)q_offset(B) + 2 * kQBytes + (size_t)n_st * kStageBytes;
   }
 };
 
@@ -85,16 +91,17 @@ __device__ __forceinline__ int tile_sequence(const int* prefix, int B, int t) {
 }
 
 template <int NH, int NPAD>
-__global__ void __launch_bounds__(kThreadsI, 1)
+__global__ void __launch_bounds__(kThreadsI, 2)
 indexer_q8_kernel(const __grid_constant__ CUtensorMap tm_ki, const Q8IndexerArgs a, int n_st, int q_off) {
   using Lay = LayoutI<NH, NPAD>;
+  constexpr int kAcc = Lay::kAcc;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem);
   uint64_t* empty = full + kMaxStagesI;
   uint64_t* tfull = empty + kMaxStagesI;
-  uint64_t* tempty = tfull + kAcc;
-  uint64_t* qfull = tempty + kAcc;
+  uint64_t* tempty = tfull + kMaxAcc;
+  uint64_t* qfull = tempty + kMaxAcc;
   uint64_t* qempty = qfull + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kSlotOffset);
   float* wq = reinterpret_cast<float*>(smem + kWOffset);  // [2][NPAD]: w times the query scale's inverse
@@ -108,7 +115,7 @@ indexer_q8_kernel(const __grid_constant__ CUtensorMap tm_ki, const Q8IndexerArgs
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < n_st; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
     for (int c = 0; c < kAcc; ++c) { mbar_init(&tfull[c], 1); mbar_init(&tempty[c], 4); }
-    // a query buffer is free once its MMAs are done and the four epilogue warps hold its weights
+    // a query buffer is free once its MMAs are done and the four epilogue warps have passed its tiles
     for (int c = 0; c < 2; ++c) { mbar_init(&qfull[c], 2); mbar_init(&qempty[c], 5); }
     fence_mbar_init();
     tma_prefetch_desc(&tm_ki);
@@ -142,20 +149,28 @@ indexer_q8_kernel(const __grid_constant__ CUtensorMap tm_ki, const Q8IndexerArgs
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  // this CTA's tiles [g_beg, g_end), and the sequence of the first
   const int total = prefix[a.B];
+  const int g_beg = (int)((int64_t)total * blockIdx.x / gridDim.x);
+  const int g_end = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
+  int b = g_beg < g_end ? tile_sequence(prefix, a.B, g_beg) : 0;
 
   if (warp == 0) {
     // ---------------- key tiles ----------------
     if (lane == 0) {
       int i = 0;
-      for (int g = blockIdx.x; g < total; g += gridDim.x, ++i) {
+      int64_t off = g_beg < g_end ? a.seq_off[b] : 0;
+      for (int g = g_beg; g < g_end; ++g, ++i) {
         const int s = i % n_st;
+        if (g >= prefix[b + 1]) {
+          do ++b; while (g >= prefix[b + 1]);
+          off = a.seq_off[b];
+        }
         if (!mbar_wait(&empty[s], ((i / n_st) & 1) ^ 1, kWaitLimitNs)) {
           report(a.status, kErrTimeout, kKernIndexerQ8, blockIdx.x, 0, i);
           break;
         }
-        const int b = tile_sequence(prefix, a.B, g);
-        const int64_t row = a.seq_off[b] + (int64_t)(g - prefix[b]) * kTile;
+        const int64_t row = off + (int64_t)(g - prefix[b]) * kTile;
         mbar_arrive_expect_tx(&full[s], Lay::kStageBytes);
 #pragma unroll
         for (int h = 0; h < NH; ++h)
@@ -168,16 +183,17 @@ indexer_q8_kernel(const __grid_constant__ CUtensorMap tm_ki, const Q8IndexerArgs
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
     if (lane == 0) {
-      constexpr uint32_t idesc = idesc_e4m3(128, NPAD);
-      int i = 0, cur_b = -1, nseq = 0;
-      for (int g = blockIdx.x; g < total; g += gridDim.x, ++i) {
+      constexpr uint32_t idesc = idesc_e4m3(128, Lay::kCols);
+      int nseq = 0;
+      bool fresh = true;  // the next tile is its sequence's first here
+      for (int g = g_beg, i = 0; g < g_end; ++g, ++i) {
         const int s = i % n_st, c = i % kAcc;
-        const int b = tile_sequence(prefix, a.B, g);
+        while (g >= prefix[b + 1]) ++b, fresh = true;
         bool ok = true;
-        if (b != cur_b) {
+        if (fresh) {
           if (nseq > 0) umma_commit(&qempty[(nseq - 1) & 1]);  // the last sequence's products
           ok = mbar_wait(&qfull[nseq & 1], (nseq >> 1) & 1, kWaitLimitNs);
-          cur_b = b;
+          fresh = false;
           ++nseq;
         }
         if (!ok || !mbar_wait(&full[s], (i / n_st) & 1, kWaitLimitNs) ||
@@ -188,18 +204,15 @@ indexer_q8_kernel(const __grid_constant__ CUtensorMap tm_ki, const Q8IndexerArgs
         tc_fence_after();
         const uint32_t a_base = smem_u32(ring + s * Lay::kStageBytes);
         const uint32_t b_base = smem_u32(qbuf + ((nseq - 1) & 1) * Lay::kQBytes);
-        const uint32_t d = tmem_base + c * NPAD;
+        const uint32_t d = tmem_base + c * Lay::kCols;
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
-#pragma unroll
-          for (int k = 0; k < NH * 4; ++k) {
-            if (k >= ksteps) break;
-            const int h = k / 4, kk = k % 4;
-            const uint64_t ad = umma_desc_sw128(a_base + h * kTile * 128 + kk * 32, 16, 1024);
-            const uint64_t bd =
-                umma_desc_sw128(b_base + part * Lay::kPartBytes + h * NPAD * 128 + kk * 32, 16, 1024);
-            umma_e4m3(d, ad, bd, idesc, (part | k) != 0);
-          }
+        for (int k = 0; k < NH * 4; ++k) {
+          if (k >= ksteps) break;
+          const int h = k / 4, kk = k % 4;
+          const uint64_t ad = umma_desc_sw128(a_base + h * kTile * 128 + kk * 32, 16, 1024);
+          const uint64_t bd = umma_desc_sw128(b_base + h * Lay::kQHalf + kk * 32, 16, 1024);
+          umma_e4m3(d, ad, bd, idesc, k != 0);
+        }
         umma_commit(&empty[s]);
         umma_commit(&tfull[c]);
       }
@@ -208,59 +221,67 @@ indexer_q8_kernel(const __grid_constant__ CUtensorMap tm_ki, const Q8IndexerArgs
     // ---------------- epilogue: ReLU, head weights, sum, key scale ----------------
     const int quarter = warp & 3;  // TMEM lanes this warp may read
     const int r = quarter * 32 + lane;
-    int i = 0, cur_b = -1, nseq = 0;
-    Q8Seq seq{};
-    float wr[NPAD];
-    for (int g = blockIdx.x; g < total; g += gridDim.x, ++i) {
+    int nseq = 0;
+    bool fresh = true;
+    Q8Seq seq = q8_seq(a.seq_off, a.seq_len, b, a.n_tokens, a.S_max);
+    // scale of this thread's key of tile g of the sequence: loaded a tile ahead
+    auto key_scale = [&](int t) { return t < seq.len ? __ldcg(&a.scales[(seq.off + t) / kQ8Block]) : 0.f; };
+    float ks = g_beg < g_end ? key_scale((g_beg - prefix[b]) * kTile + r) : 0.f;
+    for (int g = g_beg, i = 0; g < g_end; ++g, ++i) {
       const int c = i % kAcc;
-      const int b = tile_sequence(prefix, a.B, g);
       bool ok = true;
-      if (b != cur_b) {
-        if (lane == 0) ok = mbar_wait(&qfull[nseq & 1], (nseq >> 1) & 1, kWaitLimitNs);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        __syncwarp();
-        if (ok) {
-#pragma unroll
-          for (int j = 0; j < NPAD; ++j) wr[j] = wq[(nseq & 1) * NPAD + j];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&qempty[nseq & 1]);
-        }
+      if (g >= prefix[b + 1]) {
+        do ++b; while (g >= prefix[b + 1]);
         seq = q8_seq(a.seq_off, a.seq_len, b, a.n_tokens, a.S_max);
-        cur_b = b;
-        ++nseq;
+        ks = key_scale((g - prefix[b]) * kTile + r);
+        fresh = true;
       }
       const int t = (g - prefix[b]) * kTile + r;
-      float ks = 0.f;
-      if (t < seq.len) ks = __ldcg(&a.scales[(seq.off + t) / kQ8Block]);
-      if (lane == 0 && ok) ok = mbar_wait(&tfull[c], (i / kAcc) & 1, kWaitLimitNs);
+      const float ks_next = key_scale(t + kTile);
+      if (lane == 0) {
+        if (fresh) {
+          if (nseq > 0) mbar_arrive(&qempty[(nseq - 1) & 1]);
+          ok = mbar_wait(&qfull[nseq & 1], (nseq >> 1) & 1, kWaitLimitNs);
+        }
+        if (ok) ok = mbar_wait(&tfull[c], (i / kAcc) & 1, kWaitLimitNs);
+      }
       if (!__shfl_sync(0xffffffffu, ok, 0)) {
         if (lane == 0) report(a.status, kErrTimeout, kKernIndexerQ8, blockIdx.x, 2, i);
         break;
       }
+      if (fresh) ++nseq;
+      fresh = false;
       tc_fence_after();
-      uint32_t v[NPAD];
+      const float* w = wq + ((nseq - 1) & 1) * NPAD;
+      const uint32_t acc_col = tmem_base + ((uint32_t)(quarter * 32) << 16) + c * Lay::kCols;
+      float acc = 0.f;
+#pragma unroll 1  // 16 heads at a time: more would spill
+      for (int j0 = 0; j0 < NPAD; j0 += 16) {
+        uint32_t v[32];  // 16 heads of the hi part, then of the lo part (or 8 of each)
+        tmem_ld16(acc_col + j0, v);
+        if (NPAD > 8) tmem_ld16(acc_col + NPAD + j0, v + 16);
+        tmem_wait_ld();
+        constexpr int kN = NPAD > 8 ? 16 : 8;
 #pragma unroll
-      for (int j = 0; j < NPAD; j += 16)
-        tmem_ld16(tmem_base + ((uint32_t)(quarter * 32) << 16) + c * NPAD + j, &v[j]);
-      tmem_wait_ld();
+        for (int j = 0; j < kN; j += 4) {
+          const float4 wj = *reinterpret_cast<const float4*>(w + j0 + j);
+          const float ww[4] = {wj.x, wj.y, wj.z, wj.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            acc = fmaf(ww[u], fmaxf(__uint_as_float(v[j + u]) + __uint_as_float(v[kN + j + u]), 0.f), acc);
+        }
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&tempty[c]);
-      if (t < seq.len) {
-        float acc = 0.f;
-#pragma unroll
-        for (int j = 0; j < NPAD; ++j)
-          if (j < a.H_I) acc = fmaf(wr[j], fmaxf(__uint_as_float(v[j]), 0.f), acc);
-        a.scores[(int64_t)b * a.ld + t] = __fadd_rn(acc * ks, 0.f);  // canonical +0
-      }
+      if (t < seq.len) a.scores[(int64_t)b * a.ld + t] = __fadd_rn(acc * ks, 0.f);  // canonical +0
+      ks = ks_next;
     }
   } else {
     // ---------------- queries: scale, split, swizzled K-major tiles ----------------
-    int cur_b = -1, nseq = 0;
-    for (int g = blockIdx.x; g < total; g += gridDim.x) {
-      const int b = tile_sequence(prefix, a.B, g);
-      if (b == cur_b) continue;
-      cur_b = b;
+    int nseq = 0;
+    for (; g_beg < g_end && b < a.B && prefix[b] < g_end; ++b) {
+      if (prefix[b + 1] <= g_beg || prefix[b + 1] == prefix[b]) continue;  // no tiles here
       bool ok = true;
       if (lane == 0) ok = mbar_wait(&qempty[nseq & 1], ((nseq >> 1) & 1) ^ 1, kWaitLimitNs);
       if (!__shfl_sync(0xffffffffu, ok, 0)) {
@@ -268,15 +289,17 @@ indexer_q8_kernel(const __grid_constant__ CUtensorMap tm_ki, const Q8IndexerArgs
         break;
       }
       uint8_t* hi = qbuf + (nseq & 1) * Lay::kQBytes;
-      uint8_t* lo = hi + Lay::kPartBytes;
-      for (int j = warp - 6; j < a.H_I; j += 2) {
+      uint8_t* lo = hi + NPAD * 128;
+      for (int j = warp - 6; j < NPAD; j += 2) {
+        // a padding head is zero: its columns add nothing
         const uint16_t* q = a.qI + ((int64_t)b * a.H_I + j) * a.d_I;
         float x[NH][4];  // dims 4 * lane .. of each half
         uint32_t mx = 0;
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
           const int dim = h * 128 + lane * 4;
-          const uint2 v = dim < a.d_I ? __ldcg(reinterpret_cast<const uint2*>(q + dim)) : make_uint2(0u, 0u);
+          const uint2 v =
+              j < a.H_I && dim < a.d_I ? __ldcg(reinterpret_cast<const uint2*>(q + dim)) : make_uint2(0u, 0u);
           x[h][0] = __uint_as_float(v.x << 16);
           x[h][1] = __uint_as_float(v.x & 0xffff0000u);
           x[h][2] = __uint_as_float(v.y << 16);
@@ -299,11 +322,13 @@ indexer_q8_kernel(const __grid_constant__ CUtensorMap tm_ki, const Q8IndexerArgs
           const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&p0));
           const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&p1));
           const uint32_t cl = q8_from_float4(y[0] - f0.x, y[1] - f0.y, y[2] - f1.x, y[3] - f1.y);
-          const uint32_t to = h * NPAD * 128 + sw128_offset(j, lane >> 2) + (lane & 3) * 4;
+          const uint32_t to = h * Lay::kQHalf + sw128_offset(j, lane >> 2) + (lane & 3) * 4;
           *reinterpret_cast<uint32_t*>(hi + to) = ch;
           *reinterpret_cast<uint32_t*>(lo + to) = cl;
         }
-        if (lane == 0) wq[(nseq & 1) * NPAD + j] = __ldcg(&a.w[(int64_t)b * a.H_I + j]) * __uint_as_float(sb);
+        if (lane == 0)
+          wq[(nseq & 1) * NPAD + j] =
+              j < a.H_I ? __ldcg(&a.w[(int64_t)b * a.H_I + j]) * __uint_as_float(sb) : 0.f;
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -324,29 +349,35 @@ template <int NH, int NPAD>
 cudaError_t launch_nh(const Q8IndexerArgs& a, const CUtensorMap& tm_ki, int num_sms, cudaStream_t stream) {
   using Lay = LayoutI<NH, NPAD>;
   auto kern = indexer_q8_kernel<NH, NPAD>;
-  if (Lay::stages(a.B) < 2) return cudaErrorInvalidValue;  // the prefix table would crowd out the ring
-  const size_t smem = Lay::smem_bytes(a.B);
+  // two CTAs an SM where each has four stages or more, else one with all there is
+  const int half = Lay::stages(a.B, kSmemHalfI);
+  const int per_sm = half >= 4 ? 2 : 1;
+  const int n_st = per_sm == 2 ? half : Lay::stages(a.B, kSmemMaxI);
+  if (n_st < 2) return cudaErrorInvalidValue;  // the prefix table would crowd out the ring
+  const size_t smem = Lay::smem_bytes(a.B, n_st);
   cudaError_t e = ensure_smem(kern, smem);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t)a.B * ((a.S_max + kTile - 1) / kTile);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles < num_sms ? tiles : num_sms));
+  const int64_t ctas = (int64_t)num_sms * per_sm;
+  cfg.gridDim = dim3((unsigned)(tiles < ctas ? tiles : ctas));
   cfg.blockDim = dim3(kThreadsI);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1] = {pdl_attribute()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kern, tm_ki, a, Lay::stages(a.B), Lay::q_offset(a.B));
+  e = cudaLaunchKernelEx(&cfg, kern, tm_ki, a, n_st, Lay::q_offset(a.B));
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_indexer_q8(const Q8IndexerArgs& a, const CUtensorMap& tm_ki, int num_sms, cudaStream_t stream) {
-  const int nh = (a.d_I + 127) / 128, npad = (a.H_I + 15) / 16 * 16;
+  const int nh = (a.d_I + 127) / 128, npad = a.H_I <= 8 ? 8 : (a.H_I + 15) / 16 * 16;
 #define SA_IDX_CASE(NH, NP) \
   if (nh == NH && npad == NP) return launch_nh<NH, NP>(a, tm_ki, num_sms, stream);
+  SA_IDX_CASE(1, 8) SA_IDX_CASE(2, 8)
   SA_IDX_CASE(1, 16) SA_IDX_CASE(1, 32) SA_IDX_CASE(1, 48) SA_IDX_CASE(1, 64)
   SA_IDX_CASE(2, 16) SA_IDX_CASE(2, 32) SA_IDX_CASE(2, 48) SA_IDX_CASE(2, 64)
 #undef SA_IDX_CASE
