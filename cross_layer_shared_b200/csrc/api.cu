@@ -1352,6 +1352,7 @@ sa_status sa_cache_read_q8(const void* K8, const float* K_scale, const void* V8,
   a.out[0] = K;
   a.out[1] = V;
   a.out_f32 = out_dtype == SA_F32;
+  a.out_wide = aligned(K, 32) && aligned(V, 32);
   a.status = status_of(ws);
   const cudaError_t e = sa::launch_cache_read_q8(a, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail("sa_cache_read_q8 launch", e);

@@ -135,20 +135,35 @@ __global__ void __launch_bounds__(kThreadsC) cache_append_q8_kernel(const Q8Appe
 }
 
 // ---------------------------------------------------------------- reading back
-// One CTA per (sequence, 64 tokens or index entries, head, tensor).  A thread
-// takes 8 codes at a time: 8 bytes in, 16 (bf16) or 32 (fp32) out.  A code
-// times its scale is exact in fp32; bf16 rounds it only below 2^-133.
-template <bool F32>
+// A thread takes kReadPer pieces of 16 codes, all their loads before the first
+// conversion: 16 bytes in, 32 (bf16) or 64 (fp32) out, in whole 32-byte
+// sectors.  A CTA takes kReadPieces consecutive pieces of one (sequence, head,
+// tensor), so the split needs no whole rows.  A code times its scale is exact
+// in fp32; bf16 rounds it only below 2^-133.
+constexpr int kReadPer = 4;
+constexpr int kReadPieces = kReadPer * kThreadsC;
+
+__device__ __forceinline__ void store32(void* p, const uint32_t* v, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {  // an output that starts between two sectors
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+template <bool F32, int D>
 __global__ void __launch_bounds__(kThreadsC) cache_read_q8_kernel(const Q8ReadArgs a) {
+  constexpr int kPieces = D / 16;
   const int tid = threadIdx.x;
   const int b = blockIdx.z, h = blockIdx.y % a.Hkv, which = blockIdx.y / a.Hkv;
-  const int e0 = blockIdx.x * kQ8Block;
   pdl_trigger();
   pdl_wait();
   const Q8Seq s = q8_seq(a.seq_off, a.seq_len, b, a.n_tokens, a.S_max);
   const bool first = tid == 0 && blockIdx.x == 0 && blockIdx.y == 0;
   if (!s.ok && first) report(a.status, kErrDevice, kKernCacheQ8, b, s.len, s.cap);
-  const int pieces = a.d / 8;
   const int64_t row0 = s.off * a.Hkv + (int64_t)h * s.cap;
   int n;           // entries of this sequence
   int64_t out0;    // its first output row for this head
@@ -165,46 +180,65 @@ __global__ void __launch_bounds__(kThreadsC) cache_read_q8_kernel(const Q8ReadAr
     }
     out0 = o * a.Hkv + (int64_t)h * s.len;
   }
-  const int m = min(n - e0, kQ8Block);
-  for (int i = tid; i < m * pieces; i += kThreadsC) {
-    const int e = e0 + i / pieces, p = i % pieces;
-    int t = e;
-    if (a.idx) {
-      t = __ldcg(&a.idx[(int64_t)b * a.k + e]);
-      if (t >= s.len) {
-        if (p == 0 && blockIdx.y == 0) report(a.status, kErrDevice, kKernCacheQ8, (int64_t)b * a.k + e, t, s.len);
-        t = -1;
-      }
-    }
-    float v[8] = {};
-    if (t >= 0) {
-      const int64_t row = row0 + t;
-      const uint2 c = __ldcg(reinterpret_cast<const uint2*>(a.cache.codes[which] + row * a.d + p * 8));
-      const float sc = __ldcg(a.cache.scales[which] + row / kQ8Block);
-      const uint32_t q[2] = {c.x, c.y};
+  const int64_t base = (int64_t)blockIdx.x * kReadPieces;
+  const int64_t e_base = base / kPieces;
+  const int rem = (int)(base % kPieces);
+  const uint8_t* codes = a.cache.codes[which];
+  const float* scales = a.cache.scales[which];
+  int e[kReadPer], t[kReadPer];  // entry, token (-1: zeros)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        uint32_t l, u;
-        q8_to_half4(q[j], l, u);
-        const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&l));
-        const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&u));
-        v[4 * j] = f0.x * sc;
-        v[4 * j + 1] = f0.y * sc;
-        v[4 * j + 2] = f1.x * sc;
-        v[4 * j + 3] = f1.y * sc;
+  for (int i = 0; i < kReadPer; ++i) {
+    const int64_t at = e_base + (rem + tid + i * kThreadsC) / kPieces;
+    e[i] = at < n ? (int)at : -1;
+    t[i] = e[i];
+    if (a.idx && e[i] >= 0) t[i] = __ldcg(&a.idx[(int64_t)b * a.k + e[i]]);
+  }
+  uint4 c[kReadPer];
+  float sc[kReadPer];
+#pragma unroll
+  for (int i = 0; i < kReadPer; ++i) {
+    const int p = (rem + tid + i * kThreadsC) % kPieces;
+    if (t[i] >= s.len) {
+      if (p == 0 && blockIdx.y == 0)
+        report(a.status, kErrDevice, kKernCacheQ8, (int64_t)b * a.k + e[i], t[i], s.len);
+      t[i] = -1;
+    }
+    c[i] = make_uint4(0, 0, 0, 0);
+    sc[i] = 0.f;
+    if (t[i] >= 0) {
+      c[i] = __ldcg(reinterpret_cast<const uint4*>(codes + (row0 + t[i]) * D + p * 16));
+      sc[i] = __ldcg(scales + (row0 + t[i]) / kQ8Block);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kReadPer; ++i) {
+    if (e[i] < 0) continue;
+    const int p = (rem + tid + i * kThreadsC) % kPieces;
+    const uint32_t q[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+    const int64_t at = (out0 + e[i]) * D + p * 16;
+    uint32_t w[F32 ? 16 : 8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t l, u;
+      q8_to_half4(q[j], l, u);
+      const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&l));
+      const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&u));
+      const float v[4] = {f0.x * sc[i], f0.y * sc[i], f1.x * sc[i], f1.y * sc[i]};
+      if (F32) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) w[4 * j + x] = __float_as_uint(v[x]);
+      } else {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[2 * j + x]) : "f"(v[2 * x + 1]), "f"(v[2 * x]));
       }
     }
-    const int64_t at = (out0 + e) * a.d + p * 8;
     if (F32) {
-      float4* o = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out[which]) + at);
-      o[0] = make_float4(v[0], v[1], v[2], v[3]);
-      o[1] = make_float4(v[4], v[5], v[6], v[7]);
+      float* o = reinterpret_cast<float*>(a.out[which]) + at;
+      store32(o, w, a.out_wide);
+      store32(o + 8, w + (F32 ? 8 : 0), a.out_wide);
     } else {
-      uint32_t w[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(v[2 * j + 1]), "f"(v[2 * j]));
-      *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out[which]) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+      store32(reinterpret_cast<uint16_t*>(a.out[which]) + at, w, a.out_wide);
     }
   }
 }
@@ -238,10 +272,15 @@ cudaError_t launch_cache_append_q8(const Q8AppendArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_cache_read_q8(const Q8ReadArgs& a, cudaStream_t stream) {
-  const int n = a.idx ? a.k : a.S_max;
-  const dim3 grid((n + kQ8Block - 1) / kQ8Block, a.Hkv * (a.cache.codes[1] ? 2 : 1), a.B);
-  return a.out_f32 ? launch_grid(cache_read_q8_kernel<true>, a, grid, stream)
-                   : launch_grid(cache_read_q8_kernel<false>, a, grid, stream);
+  const int64_t pieces = (int64_t)(a.idx ? a.k : a.S_max) * (a.d / 16);
+  const dim3 grid((unsigned)((pieces + kReadPieces - 1) / kReadPieces), a.Hkv * (a.cache.codes[1] ? 2 : 1), a.B);
+#define SA_READ_CASE(DD)                                                                     \
+  if (a.d == DD)                                                                             \
+    return a.out_f32 ? launch_grid(cache_read_q8_kernel<true, DD>, a, grid, stream)          \
+                     : launch_grid(cache_read_q8_kernel<false, DD>, a, grid, stream);
+  SA_READ_CASE(64) SA_READ_CASE(128) SA_READ_CASE(192) SA_READ_CASE(256)
+#undef SA_READ_CASE
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace sa

@@ -106,7 +106,7 @@ struct Q8ReadArgs {
   const int64_t* out_off;  // whole sequences: [B+1] token offsets in the packed output
   int64_t n_out;
   void* out[2];
-  int out_f32;
+  int out_f32, out_wide;   // out_wide: both outputs are 32-byte aligned
   DeviceStatus* status;
 };
 cudaError_t launch_cache_read_q8(const Q8ReadArgs& a, cudaStream_t stream);
