@@ -1411,7 +1411,8 @@ sa_status sa_decode_attn_q8(const void* Q, const void* K8, const float* K_scale,
   if (!(scale > 0.f && scale < INFINITY)) return fail(SA_ERR_INVALID_ARG, "%s: scale must be finite and > 0", who);
   const int R = L_g * (Hq / Hkv);
   const sa::Q8AttnPlan p = sa::plan_attn_q8(R, B, Hkv, n_tokens, S_max, k, num_sms(), kSmallMaxCounters);
-  if ((int64_t)p.units * p.n_split >= (1ll << 31)) return fail(SA_ERR_UNSUPPORTED, "%s: too many rows", who);
+  if ((int64_t)p.units * p.n_split >= (1ll << 31) || (int64_t)L_g * B * Hq >= (1ll << 31))
+    return fail(SA_ERR_UNSUPPORTED, "%s: too many rows", who);
   if ((st = check_ws(ws, ws_bytes, SA_WS_HEADER_BYTES + sa::attn_q8_scratch_bytes(p), who)) != SA_OK) return st;
   sa::Q8AttnArgs a{};
   a.Q = reinterpret_cast<const uint16_t*>(Q);
@@ -1439,7 +1440,7 @@ sa_status sa_decode_attn_q8(const void* Q, const void* K8, const float* K_scale,
   a.cnt = reinterpret_cast<uint32_t*>(base + kSmallCounterOffset);
   a.po = reinterpret_cast<float*>(base + SA_WS_HEADER_BYTES);
   a.pml = reinterpret_cast<float2*>(base + SA_WS_HEADER_BYTES +
-                                    round_up((size_t)p.units * p.n_split * p.rows * 128 * 4, 256));
+                                    round_up((size_t)p.units * p.parts * p.rows * 128 * 4, 256));
   a.status = status_of(ws);
   const cudaError_t e = sa::launch_attn_q8(a, p, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail("sa_decode_attn_q8 launch", e);

@@ -519,6 +519,11 @@ Q8AttnPlan plan_attn_q8(int R, int B, int Hkv, int64_t n_tokens, int S_max, int 
   p.rows = padded_rows(R);
   p.units = B * Hkv * p.row_tiles;
   const int64_t n = k > 0 ? k : S_max;  // keys of the longest unit
+  p.group = R > kQ8GroupRows;
+  if (p.group) {
+    plan_attn_q8_group(p, n, sms);
+    return p;
+  }
   // keys a CTA takes per round of all its key groups
   const int round = kKeysQ * (p.rows <= 16 ? kWarpsQ : kWarpsQ * 16 / p.rows);
   const int64_t slots = 2ll * sms;      // CTAs the GPU holds at once
@@ -538,16 +543,18 @@ Q8AttnPlan plan_attn_q8(int R, int B, int Hkv, int64_t n_tokens, int S_max, int 
   p.chunk = (int)chunk;
   p.n_split = (int)((n + chunk - 1) / chunk);
   if (p.n_split < 1) p.n_split = 1;
+  p.parts = p.n_split;
   return p;
 }
 
 size_t attn_q8_scratch_bytes(const Q8AttnPlan& p) {
-  if (p.n_split <= 1) return 0;
-  const size_t n = (size_t)p.units * p.n_split * p.rows;
+  if (p.parts <= 1) return 0;
+  const size_t n = (size_t)p.units * p.parts * p.rows;
   return (n * kDq * 4 + 255) / 256 * 256 + (n * 8 + 255) / 256 * 256;
 }
 
 cudaError_t launch_attn_q8(const Q8AttnArgs& a, const Q8AttnPlan& p, cudaStream_t stream) {
+  if (p.group) return launch_attn_q8_group(a, p, stream);
   switch (p.rows) {
     case 8: return launch_nt<1, 1>(a, p, stream);
     case 16: return launch_nt<2, 1>(a, p, stream);

@@ -156,10 +156,17 @@ struct Q8AttnArgs {
   DeviceStatus* status;
 };
 struct Q8AttnPlan {
-  int row_tiles, units, n_split, chunk, rows;  // rows: query rows a unit stores (padded)
+  bool group;  // attn_q8_group.cu
+  int row_tiles, units, n_split, chunk;
+  int parts, rows;  // partial results of a unit, and the query rows of each (padded)
 };
 Q8AttnPlan plan_attn_q8(int R, int B, int Hkv, int64_t n_tokens, int S_max, int k, int sms, int max_counters);
 size_t attn_q8_scratch_bytes(const Q8AttnPlan& p);
 cudaError_t launch_attn_q8(const Q8AttnArgs& a, const Q8AttnPlan& p, cudaStream_t stream);
+
+// ---- attn_q8_group.cu: more than kQ8GroupRows query rows per (b, g) ----
+constexpr int kQ8GroupRows = 16;
+void plan_attn_q8_group(Q8AttnPlan& p, int64_t n, int sms);
+cudaError_t launch_attn_q8_group(const Q8AttnArgs& a, const Q8AttnPlan& p, cudaStream_t stream);
 
 }  // namespace sa
