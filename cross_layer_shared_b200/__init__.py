@@ -789,46 +789,72 @@ def block_union_prefill_noalloc(idx, q_pos, Q, K, V, block: int, scale: float, k
 Q8_BLOCK = 64
 
 
-def _same_device(dev: torch.device, *tensors) -> None:
-    """The kernels run on the current device: every tensor has to be there."""
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {dev}, the current device is cuda:{torch.cuda.current_device()}"
-                         if dev.type == "cuda" else f"tensors must be on the GPU, not on {dev}")
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors are on {dev} and on {t.device}")
+def _on(t: torch.Tensor, dtype, dev: int, name: str) -> int:
+    """Address of a contiguous tensor of dtype on GPU dev."""
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of {dtype} on GPU {dev}, not {t.dtype} on {t.device}")
+    return t.data_ptr()
 
 
-def _cache_q8(codes, scales, Hkv: int, d: int, name: str) -> int:
-    """Checks one 8-bit cache; returns its token places."""
-    _dev(codes, torch.float8_e4m3fn, name)
-    _dev(scales, torch.float32, f"{name}'s scales")
-    if Hkv < 1 or d < 1 or codes.shape[-1] != d or codes.numel() % (Hkv * d * Q8_BLOCK):
+def _sized(t: torch.Tensor, shape, dtype, dev: int, name: str) -> int:
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    return _on(t, dtype, dev, name)
+
+
+def _current(t: torch.Tensor, name: str) -> int:
+    """Index of t's GPU, which has to be the current one: the kernels run there."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current GPU, not on {t.device}")
+    return dev
+
+
+def _code(t: torch.Tensor, name: str) -> int:
+    if t.dtype is torch.bfloat16:
+        return SA_BF16
+    if t.dtype is torch.float32:
+        return SA_F32
+    raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, not {t.dtype}")
+
+
+def _cache_q8(codes, scales, Hkv: int, d: int, dev: int, name: str):
+    """Checks one 8-bit cache; returns its addresses and token places."""
+    n = codes.numel()
+    n_tokens = n // (Hkv * d) if Hkv > 0 and d > 0 else 0
+    if codes.shape[-1] != d or n_tokens % Q8_BLOCK or n != n_tokens * Hkv * d:
         raise ValueError(f"{name} must be [.., {d}] with a multiple of {Q8_BLOCK} token places of {Hkv} heads, not "
                          f"{tuple(codes.shape)}")
-    n_tokens = codes.numel() // (Hkv * d)
     if scales.numel() != n_tokens * Hkv // Q8_BLOCK:
         raise ValueError(f"{name}'s scales must be {n_tokens * Hkv // Q8_BLOCK} values, not {scales.numel()}")
-    return n_tokens
+    return _on(codes, torch.float8_e4m3fn, dev, name), _on(scales, torch.float32, dev, f"{name}'s scales"), n_tokens
 
 
-def _pair_q8(K8, K_scale, V8, V_scale, Hkv: int, d: int) -> int:
-    n_tokens = _cache_q8(K8, K_scale, Hkv, d, "K8")
-    if (V8 is None) != (V_scale is None):
+def _pair_q8(K8, K_scale, V8, V_scale, Hkv: int, d: int, dev: int):
+    k, ks, n_tokens = _cache_q8(K8, K_scale, Hkv, d, dev, "K8")
+    if V8 is None and V_scale is None:
+        return k, ks, None, None, n_tokens
+    if V8 is None or V_scale is None:
         raise ValueError("V8 and V_scale go together")
-    if V8 is not None and _cache_q8(V8, V_scale, Hkv, d, "V8") != n_tokens:
+    v, vs, n = _cache_q8(V8, V_scale, Hkv, d, dev, "V8")
+    if n != n_tokens:
         raise ValueError("K8 and V8 must have one size")
-    return n_tokens
+    return k, ks, v, vs, n_tokens
 
 
-def _new_rows(x, name: str, dtype=None) -> int:
-    """New tokens' rows [n, Hkv, d], each row of heads contiguous; returns the rows' stride in elements."""
-    if not (x.is_cuda and x.dim() == 3 and x.dtype in (torch.bfloat16, torch.float32)):
-        raise ValueError(f"{name} must be a CUDA tensor [n, Hkv, d] of torch.bfloat16 or torch.float32")
+def _new_rows(x: torch.Tensor, dev: int, name: str):
+    """Address of new tokens' rows [n, Hkv, d], each row of heads contiguous, and their stride in elements."""
+    if x.get_device() != dev:
+        raise ValueError(f"{name} must be on GPU {dev}, not on {x.device}")
     n, Hkv, d = x.shape
-    if x.numel() and ((d > 1 and x.stride(2) != 1) or (Hkv > 1 and x.stride(1) != d)):
+    s0, s1, s2 = x.stride()
+    if (s2 != 1 and d > 1 or s1 != d and Hkv > 1) and x.numel():
         raise ValueError(f"each token's [Hkv, d] of {name} must be contiguous")
-    return x.stride(0) if n > 1 else Hkv * d
+    return x.data_ptr(), s0 if n > 1 else Hkv * d
+
+
+def _header_ws(ws, dev: int) -> torch.Tensor:
+    return workspace(WS_HEADER_BYTES, f"cuda:{dev}") if ws is None else ws
 
 
 def cache_append_q8(new_K, new_V, K8, K_scale, V8, V_scale, seq_off, seq_len, new_off=None,
@@ -840,33 +866,33 @@ def cache_append_q8(new_K, new_V, K8, K_scale, V8, V_scale, seq_off, seq_len, ne
     [B+1]; None: one row per sequence) and land behind the tokens there:
     seq_len already counts them.  max_new: host bound of a sequence's new
     rows (default: n).  One tensor: new_V = V8 = V_scale = None."""
-    B = seq_len.shape[0]
-    sK = _new_rows(new_K, "new_K")
+    dev = _current(new_K, "new_K")
+    code = _code(new_K, "new_K")
+    k, sK = _new_rows(new_K, dev, "new_K")
     n, Hkv, d = new_K.shape
+    B = seq_len.shape[0]
     if (new_V is None) != (V8 is None):
         raise ValueError("new_V and V8 go together")
-    sV = 0
+    v, sV = None, 0
     if new_V is not None:
-        sV = _new_rows(new_V, "new_V")
-        if new_V.shape != new_K.shape or new_V.dtype != new_K.dtype:
+        if new_V.shape != new_K.shape or new_V.dtype is not new_K.dtype:
             raise ValueError("new_K and new_V must have one shape and dtype")
-    n_tokens = _pair_q8(K8, K_scale, V8, V_scale, Hkv, d)
-    _seqs(seq_off, seq_len, B)
+        v, sV = _new_rows(new_V, dev, "new_V")
+    K8p, Ksp, V8p, Vsp, n_tokens = _pair_q8(K8, K_scale, V8, V_scale, Hkv, d, dev)
+    off = None
     if new_off is None:
         if n != B:
             raise ValueError(f"without new_off every sequence gets one row: new_K must have {B} rows, not {n}")
         max_new = 1
     else:
-        _out(new_off, (B + 1,), (torch.int64,), "new_off")
-        max_new = n if max_new is None else int(max_new)
-    _same_device(K8.device, new_K, new_V, K_scale, V8, V_scale, seq_off, seq_len, new_off, ws)
-    if ws is None:
-        ws = workspace(WS_HEADER_BYTES, K8.device)
-    _ws(ws)
-    code = SA_F32 if new_K.dtype == torch.float32 else SA_BF16
-    _check(lib().sa_cache_append_q8(_ptr(new_K), sK, _ptr(new_V), sV, code, n, _ptr(new_off), max_new, _ptr(K8),
-                                    _ptr(K_scale), _ptr(V8), _ptr(V_scale), _ptr(seq_off), _ptr(seq_len), B, n_tokens,
-                                    Hkv, d, _ptr(ws), ws.numel(), _stream(stream)))
+        off = _sized(new_off, (B + 1,), torch.int64, dev, "new_off")
+        if max_new is None:
+            max_new = n
+    ws = _header_ws(ws, dev)
+    _check(lib().sa_cache_append_q8(k, sK, v, sV, code, n, off, max_new, K8p, Ksp, V8p, Vsp,
+                                    _sized(seq_off, (B + 1,), torch.int64, dev, "seq_off"),
+                                    _sized(seq_len, (B,), torch.int32, dev, "seq_len"), B, n_tokens, Hkv, d,
+                                    _on(ws, torch.uint8, dev, "ws"), ws.numel(), _stream(stream)))
 
 
 def cache_read_q8(K8, K_scale, V8, V_scale, seq_off, seq_len, S_max: int, Hkv: int, idx=None, out_off=None,
@@ -877,66 +903,60 @@ def cache_read_q8(K8, K_scale, V8, V_scale, seq_off, seq_len, S_max: int, Hkv: i
     out_off[b]*Hkv of [n_out*Hkv, d] (out_off int64 [B+1], the running sum of
     seq_len; n_out its last value, or K's).  Returns (K, V), or K alone
     without V8."""
+    dev = _current(K8, "K8")
     B, d = seq_len.shape[0], K8.shape[-1]
-    n_tokens = _pair_q8(K8, K_scale, V8, V_scale, Hkv, d)
-    _seqs(seq_off, seq_len, B)
+    K8p, Ksp, V8p, Vsp, n_tokens = _pair_q8(K8, K_scale, V8, V_scale, Hkv, d, dev)
     if (idx is None) == (out_off is None):
         raise ValueError("give either idx (picked rows) or out_off (whole sequences)")
     if V is not None and V8 is None:
         raise ValueError("V and V8 go together")
+    idxp = offp = None
     if idx is not None:
         k = idx.shape[1]
-        _out(idx, (B, k), (torch.int32,), "idx")
+        idxp = _sized(idx, (B, k), torch.int32, dev, "idx")
         n_out, shape = 0, (B, Hkv, k, d)
     else:
         k = 0
-        _out(out_off, (B + 1,), (torch.int64,), "out_off")
+        offp = _sized(out_off, (B + 1,), torch.int64, dev, "out_off")
         if n_out is None:
             if K is None:
                 raise ValueError("give n_out, the token rows of the packed output, or K")
             n_out = K.numel() // (Hkv * d)
-        n_out = int(n_out)
         shape = (n_out * Hkv, d)
     if K is None:
         K = torch.empty(shape, dtype=out_dtype, device=K8.device)
     if V8 is not None and V is None:
         V = torch.empty(shape, dtype=K.dtype, device=K8.device)
-    _out(K, shape, (torch.bfloat16, torch.float32), "K")
-    if V is not None:
-        _out(V, shape, (K.dtype,), "V")
-    _same_device(K8.device, K_scale, V8, V_scale, seq_off, seq_len, idx, out_off, K, V, ws)
-    if ws is None:
-        ws = workspace(WS_HEADER_BYTES, K8.device)
-    _ws(ws)
-    code = SA_F32 if K.dtype == torch.float32 else SA_BF16
-    _check(lib().sa_cache_read_q8(_ptr(K8), _ptr(K_scale), _ptr(V8), _ptr(V_scale), _ptr(seq_off), _ptr(seq_len), B,
-                                  n_tokens, S_max, Hkv, d, _ptr(idx), k, _ptr(out_off), n_out, _ptr(K), _ptr(V), code,
-                                  _ptr(ws), ws.numel(), _stream(stream)))
+    code = _code(K, "K")
+    ws = _header_ws(ws, dev)
+    _check(lib().sa_cache_read_q8(K8p, Ksp, V8p, Vsp, _sized(seq_off, (B + 1,), torch.int64, dev, "seq_off"),
+                                  _sized(seq_len, (B,), torch.int32, dev, "seq_len"), B, n_tokens, S_max, Hkv, d,
+                                  idxp, k, offp, n_out, _sized(K, shape, K.dtype, dev, "K"),
+                                  None if V is None else _sized(V, shape, K.dtype, dev, "V"), code,
+                                  _on(ws, torch.uint8, dev, "ws"), ws.numel(), _stream(stream)))
     return K if V8 is None else (K, V)
 
 
 def index_score_q8(qI, w, KI8, KI_scale, seq_off, seq_len, S_max: int, scores=None, ld: Optional[int] = None, ws=None,
                    stream=None) -> torch.Tensor:
     """index_score over an 8-bit key cache (sa_index_score_q8)."""
+    dev = _current(qI, "qI")
     B, H_I, d_I = qI.shape
-    _dev(qI, torch.bfloat16, "qI"), _out(w, (B, H_I), (torch.float32,), "w")
-    n_tokens = _cache_q8(KI8, KI_scale, 1, d_I, "KI8")
-    _seqs(seq_off, seq_len, B)
+    K8p, Ksp, n_tokens = _cache_q8(KI8, KI_scale, 1, d_I, dev, "KI8")
     if scores is None:
         ld = int(ld if ld is not None else max(S_max, 1))
         scores = torch.empty((B, ld), dtype=torch.float32, device=qI.device)
-    else:
-        have = _rows_out(scores, B, S_max, "scores")
-        if ld is not None and int(ld) != have:
-            raise ValueError(f"ld={ld} does not match scores of {have} columns")
-        ld = have
-    _same_device(qI.device, w, KI8, KI_scale, seq_off, seq_len, scores, ws)
-    if ws is None:
-        ws = workspace(WS_HEADER_BYTES, qI.device)
-    _ws(ws)
-    _check(lib().sa_index_score_q8(_ptr(qI), _ptr(w), _ptr(KI8), _ptr(KI_scale), _ptr(seq_off), _ptr(seq_len), B,
-                                   n_tokens, S_max, H_I, d_I, _ptr(scores), ld, _ptr(ws), ws.numel(),
-                                   _stream(stream)))
+    elif ld is not None and ld != scores.shape[-1]:
+        raise ValueError(f"ld={ld} does not match scores of {scores.shape[-1]} columns")
+    ld = scores.shape[-1]
+    if ld < S_max:
+        raise ValueError(f"scores must be [{B}, >= {S_max}], not {tuple(scores.shape)}")
+    ws = _header_ws(ws, dev)
+    _check(lib().sa_index_score_q8(_on(qI, torch.bfloat16, dev, "qI"), _sized(w, (B, H_I), torch.float32, dev, "w"),
+                                   K8p, Ksp, _sized(seq_off, (B + 1,), torch.int64, dev, "seq_off"),
+                                   _sized(seq_len, (B,), torch.int32, dev, "seq_len"), B, n_tokens, S_max, H_I, d_I,
+                                   _sized(scores, (B, ld), torch.float32, dev, "scores"), ld,
+                                   _on(ws, torch.uint8, dev, "ws"), ws.numel(), _stream(stream)))
     return scores
 
 
@@ -949,27 +969,25 @@ def decode_attn_q8(Q, K8, K_scale, V8, V_scale, seq_off, seq_len, S_max: int, Hk
     """Decode attention over 8-bit caches (sa_decode_attn_q8): Q bf16 [L, B,
     Hq, d] over the tokens of idx int32 [B, k] (shared by the L layers), or
     with idx None over every token of each sequence.  Returns O [L, B, Hq, d]."""
+    dev = _current(Q, "Q")
     L, B, Hq, d = Q.shape
-    _dev(Q, torch.bfloat16, "Q")
-    n_tokens = _pair_q8(K8, K_scale, V8, V_scale, Hkv, d)
     if V8 is None:
         raise ValueError("V8 is missing")
-    _seqs(seq_off, seq_len, B)
-    k = 0
+    K8p, Ksp, V8p, Vsp, n_tokens = _pair_q8(K8, K_scale, V8, V_scale, Hkv, d, dev)
+    k, idxp = 0, None
     if idx is not None:
         k = idx.shape[1]
-        _out(idx, (B, k), (torch.int32,), "idx")
+        idxp = _sized(idx, (B, k), torch.int32, dev, "idx")
     if O is None:
         O = torch.empty((L, B, Hq, d), dtype=out_dtype, device=Q.device)
-    _out(O, (L, B, Hq, d), (torch.bfloat16, torch.float32), "O")
-    _same_device(Q.device, K8, K_scale, V8, V_scale, seq_off, seq_len, idx, O, ws)
+    code = _code(O, "O")
     if ws is None:
         ws = workspace(decode_attn_q8_workspace_size(L, B, n_tokens, S_max, Hq, Hkv, d, k), Q.device)
-    _ws(ws)
-    code = SA_F32 if O.dtype == torch.float32 else SA_BF16
-    _check(lib().sa_decode_attn_q8(_ptr(Q), _ptr(K8), _ptr(K_scale), _ptr(V8), _ptr(V_scale), _ptr(seq_off),
-                                   _ptr(seq_len), _ptr(idx), L, B, n_tokens, S_max, Hq, Hkv, d, k, float(scale),
-                                   _ptr(O), code, _ptr(ws), ws.numel(), _stream(stream)))
+    _check(lib().sa_decode_attn_q8(_on(Q, torch.bfloat16, dev, "Q"), K8p, Ksp, V8p, Vsp,
+                                   _sized(seq_off, (B + 1,), torch.int64, dev, "seq_off"),
+                                   _sized(seq_len, (B,), torch.int32, dev, "seq_len"), idxp, L, B, n_tokens, S_max,
+                                   Hq, Hkv, d, k, scale, _sized(O, Q.shape, O.dtype, dev, "O"), code,
+                                   _on(ws, torch.uint8, dev, "ws"), ws.numel(), _stream(stream)))
     return O
 
 
