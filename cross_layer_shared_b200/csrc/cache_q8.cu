@@ -8,6 +8,13 @@
 // are read, reduces max|x|, picks the block's scale and stores the codes.  A
 // block that already holds tokens keeps its scale unless the new ones need a
 // larger one; then the CTA also moves the old codes to it.
+//
+// A CTA's block is (blockIdx.z's sequence, block blockIdx.x behind its first
+// new token) where the sequences' counts are alike.  Ragged counts would leave
+// many such CTAs without work, each a place on the GPU for the time of a load
+// (16 prompts of 517 .. 16384 tokens: half of them, 30 of 165 us); there the
+// touched blocks are numbered through, and each warp finds its CTA's block by
+// a scan over the sequences, 32 at a time.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -49,27 +56,78 @@ struct Raw8<true> {
   }
 };
 
-template <bool F32, int D>
+struct NewTokens {  // of one sequence; n = 0 when it has none or is not as described
+  Q8Seq s;
+  int64_t src0;   // first row
+  int n, first;   // count, and the first touched block
+  __device__ __forceinline__ int blocks() const { return n == 0 ? 0 : (s.len - 1) / kQ8Block - first + 1; }
+};
+
+__device__ __forceinline__ NewTokens new_tokens(const Q8AppendArgs& a, int b, bool rep) {
+  NewTokens t;
+  t.s = q8_seq(a.seq_off, a.seq_len, b, a.n_tokens, 0x7fffffff);
+  t.src0 = a.new_off ? __ldcg(reinterpret_cast<const long long*>(a.new_off) + b) : b;
+  const int64_t src1 = a.new_off ? __ldcg(reinterpret_cast<const long long*>(a.new_off) + b + 1) : b + 1;
+  const int64_t n = src1 - t.src0;
+  const bool ok = t.s.ok && n >= 0 && n <= t.s.len && n <= a.max_new && t.src0 >= 0 && src1 <= a.n_rows;
+  if (!ok && rep) report(a.status, kErrDevice, kKernCacheQ8, b, t.s.ok ? n : -1, t.s.len);
+  t.n = ok ? (int)n : 0;
+  t.first = (t.s.len - t.n) / kQ8Block;
+  return t;
+}
+
+template <bool F32, int D, bool FLAT>
 __global__ void __launch_bounds__(kThreadsC) cache_append_q8_kernel(const Q8AppendArgs a) {
   constexpr int kPieces = D / 8;                           // 8-element pieces of a row
   constexpr int kPer = kQ8Block * kPieces / kThreadsC;     // pieces a thread holds
   __shared__ uint32_t warp_max[kThreadsC / 32];
   const int tid = threadIdx.x;
-  const int b = blockIdx.z, h = blockIdx.y % a.Hkv, which = blockIdx.y / a.Hkv;
+  const int h = blockIdx.y % a.Hkv, which = blockIdx.y / a.Hkv;
   pdl_trigger();
   pdl_wait();
-  const Q8Seq s = q8_seq(a.seq_off, a.seq_len, b, a.n_tokens, 0x7fffffff);
-  const int64_t src0 = a.new_off ? __ldcg(reinterpret_cast<const long long*>(a.new_off) + b) : b;
-  const int64_t src1 = a.new_off ? __ldcg(reinterpret_cast<const long long*>(a.new_off) + b + 1) : b + 1;
-  const int64_t n = src1 - src0;
-  if (!s.ok || n < 0 || n > s.len || n > a.max_new || src0 < 0 || src1 > a.n_rows) {
-    if (tid == 0 && blockIdx.x == 0 && blockIdx.y == 0)
-      report(a.status, kErrDevice, kKernCacheQ8, b, s.ok ? n : -1, s.len);
-    return;
+  NewTokens nt;
+  int blk = blockIdx.x;  // block behind the sequence's first touched one
+  if (FLAT) {
+    const int lane = tid & 31;
+    // one CTA more than there can be blocks: it meets every sequence
+    const bool rep = blockIdx.y == 0 && blockIdx.x == gridDim.x - 1 && tid < 32;
+    bool found = false;
+    for (int base = 0; base < a.B && !found; base += 32) {
+      int cnt = 0;
+      if (base + lane < a.B) {
+        nt = new_tokens(a, base + lane, rep);
+        cnt = nt.blocks();
+      }
+      int incl = cnt;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, incl > blk);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        blk -= __shfl_sync(0xffffffffu, incl - cnt, l);
+        nt.s.off = __shfl_sync(0xffffffffu, nt.s.off, l);
+        nt.s.cap = __shfl_sync(0xffffffffu, nt.s.cap, l);
+        nt.s.len = __shfl_sync(0xffffffffu, nt.s.len, l);
+        nt.src0 = __shfl_sync(0xffffffffu, nt.src0, l);
+        nt.n = __shfl_sync(0xffffffffu, nt.n, l);
+        nt.first = __shfl_sync(0xffffffffu, nt.first, l);
+        found = true;
+      } else {
+        blk -= __shfl_sync(0xffffffffu, incl, 31);
+      }
+    }
+    if (!found) return;
+  } else {
+    nt = new_tokens(a, blockIdx.z, tid == 0 && blockIdx.x == 0 && blockIdx.y == 0);
+    if (blk >= nt.blocks()) return;
   }
-  const int pos0 = s.len - (int)n;
-  const int t0 = (pos0 / kQ8Block + (int)blockIdx.x) * kQ8Block;  // the block's first token
-  if (n == 0 || t0 >= s.len) return;
+  const Q8Seq& s = nt.s;
+  const int64_t src0 = nt.src0;
+  const int pos0 = s.len - nt.n;
+  const int t0 = (nt.first + blk) * kQ8Block;  // the block's first token
   const int lo = max(pos0 - t0, 0), hi = min(s.len - t0, kQ8Block);  // new tokens [lo, hi) of the block
   const int64_t row0 = s.off * a.Hkv + (int64_t)h * s.cap + t0;
   float* scale_p = a.cache.scales[which] + row0 / kQ8Block;
@@ -260,12 +318,20 @@ cudaError_t launch_grid(Kernel kern, const Args& a, dim3 grid, cudaStream_t stre
 
 cudaError_t launch_cache_append_q8(const Q8AppendArgs& a, cudaStream_t stream) {
   // blocks a sequence's new tokens can touch: one more than full blocks when they start inside one
-  const int blocks = (a.max_new + kQ8Block - 2) / kQ8Block + 1;
-  const dim3 grid(blocks, a.Hkv * (a.cache.codes[1] ? 2 : 1), a.B);
-#define SA_APPEND_CASE(DD)                                                                     \
-  if (a.d == DD)                                                                               \
-    return a.in_f32 ? launch_grid(cache_append_q8_kernel<true, DD>, a, grid, stream)           \
-                    : launch_grid(cache_append_q8_kernel<false, DD>, a, grid, stream);
+  const int64_t blocks = ((int64_t)a.max_new + kQ8Block - 2) / kQ8Block + 1;
+  // and all of them together: less than two more than full blocks each
+  const int64_t all = a.n_rows / kQ8Block + 2ll * a.B + 1;
+  const int units = a.Hkv * (a.cache.codes[1] ? 2 : 1);
+  const bool flat = blocks * a.B > all + all / 4;
+  const dim3 grid((unsigned)(flat ? all : blocks), units, flat ? 1 : a.B);
+#define SA_APPEND_CASE(DD)                                                                      \
+  if (a.d == DD) {                                                                              \
+    if (flat)                                                                                   \
+      return a.in_f32 ? launch_grid(cache_append_q8_kernel<true, DD, true>, a, grid, stream)    \
+                      : launch_grid(cache_append_q8_kernel<false, DD, true>, a, grid, stream);  \
+    return a.in_f32 ? launch_grid(cache_append_q8_kernel<true, DD, false>, a, grid, stream)     \
+                    : launch_grid(cache_append_q8_kernel<false, DD, false>, a, grid, stream);   \
+  }
   SA_APPEND_CASE(64) SA_APPEND_CASE(128) SA_APPEND_CASE(192) SA_APPEND_CASE(256)
 #undef SA_APPEND_CASE
   return cudaErrorInvalidValue;

@@ -628,7 +628,8 @@ sa_status sa_combine_partials(const float* O_part, int64_t o_stride, const float
  * NaN elements get the NaN code and infinite ones the largest code of the
  * block's scale; neither counts towards it.  Supported: d in {64, 128, 192,
  * 256}.  Device errors: n_b outside [0, min(max_new, seq_len[b])] or rows
- * past n_rows -> SA_ERR_DEVICE, nothing of the sequence is written. */
+ * past n_rows -> SA_ERR_DEVICE, nothing of the sequence is written (and, where
+ * rows of several sequences overlap, not all of those behind it). */
 sa_status sa_cache_append_q8(const void* new_K, int64_t stride_K, const void* new_V, int64_t stride_V,
                              sa_dtype in_dtype, int64_t n_rows, const int64_t* new_off, int max_new, void* K8,
                              float* K_scale, void* V8, float* V_scale, const int64_t* seq_off,
