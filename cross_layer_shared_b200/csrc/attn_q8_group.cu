@@ -9,7 +9,7 @@
 // halves of O in TMEM), so what is left is latency: a slice of an index is a
 // handful of tiles.
 //
-//   * Warps 9-16 (producers) load the codes of a tile straight into registers
+//   * Warps 9-12 (producers) load the codes of a tile straight into registers
 //     (16 bytes a lane, the next K and V pieces in flight while the last ones
 //     are stored), make halves of them (exact) and write them as 128-byte
 //     swizzled tiles, K as [keys, d] K-major, V the same rows read MN-major.
@@ -18,12 +18,13 @@
 //     over the consumed K tile.  The V scale joins P, not V: with l the sum of
 //     p = 2^(z - m), O sums p * (vs 2^lc).  m and lc are whole numbers, m moves
 //     when a logit passes it by 14 and lc keeps the largest p vs 2^lc between
-//     2^7 and 2^14: halves hold a weight's 11 bits, whatever the scales, and
-//     moving m costs no pass over O (lc takes it up).  fp32 outputs use two
-//     halves per weight (22 bits).
+//     2^7 and 2^14: halves hold a weight's 11 bits, however far the scales are
+//     apart, and moving m costs no pass over O (lc takes it up).  (lc stops at
+//     67: V scales below 2^-60 lose their weights' bits towards f16's
+//     subnormals.)  fp32 outputs use two halves per weight (22 bits).
 //   * Queries enter as halves scaled per row by a power of two (as in
-//     attn_q8.cu), each row and key half leaves (m, l, o / l) of its slice in
-//     the workspace, and a second kernel merges them.  It is launched with
+//     attn_q8.cu); each row leaves its slice's (m, l, o / l) in the workspace,
+//     and a second kernel merges them.  It is launched with
 //     programmatic dependence and reads one row per warp, so the merge uses
 //     the whole GPU and no counters.
 #include <cuda_fp16.h>
@@ -42,15 +43,23 @@ using namespace wm;
 
 constexpr int kDg = 128;
 constexpr int kKeysG = 128;     // keys of a tile
-constexpr int kSoftWarps = 8, kMmaWarp = 8, kProdWarp = 9, kProdWarps = 8;
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kProdWarp = 9, kProdWarps = 4;
 constexpr int kThreadsG = 32 * (kProdWarp + kProdWarps);
+constexpr int kPer = 128 * 8 / (32 * kProdWarps);  // 16-byte pieces of a K (or V) tile a producer holds
+static_assert(32 * kProdWarps == kKeysG, "one producer thread per key's scales");
+constexpr int kRowStep = 128 / kPer;
 constexpr int kHalfG = 16384;   // 128 rows x 128 bytes
 constexpr int kTileG = 2 * kHalfG;
 constexpr int kStagesG = 2;
+constexpr int kORowG = kDg + 4;  // floats of an output row in shared memory
 
-struct MetaG {
-  float ks[kKeysG], vs[kKeysG], ve[kKeysG];  // scales, and the exponent of vs
+constexpr int kMinExp = -60;
+constexpr float kMaxLc = 7.f - kMinExp;
+
+struct alignas(16) MetaG {
+  float ks[kKeysG], vs[kKeysG], ve[kKeysG];  // scales, and the exponent of vs (at least kMinExp)
   uint32_t seen[4];                          // bit c of word w: key 32w + c is a token
+  float emax[4];                             // largest ve of the word
 };
 
 template <bool PRECISE>
@@ -73,6 +82,36 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) 
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// two floats at once
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
+  return pair(__uint_as_float(lo), __uint_as_float(hi));
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
 
@@ -153,12 +192,12 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *slot;
-  const int64_t part0 = ((int64_t)unit * a.n_split + slice) * 2;  // two key halves
+  const int64_t part = (int64_t)unit * a.n_split + slice;
 
   if (warp >= kProdWarp) {
     // =============== producers ===============
     const int pt = tid - kProdWarp * 32;
-    const int pr = pt >> 3, pc = pt & 7;  // rows pr + 32 i, 16-byte piece pc
+    const int pr = pt >> 3, pc = pt & 7;  // rows pr + kRowStep i, 16-byte piece pc
     const int64_t row0 = s.off * a.Hkv + (int64_t)g * s.cap;
     const bool rep = g == 0 && rt == 0;
     // token of key r of tile j, or -1
@@ -167,15 +206,15 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
       if (e >= e_end) return -1;
       return a.idx ? __ldcg(&a.idx[(int64_t)b * a.k + e]) : e;
     };
-    auto fetch = [&](const uint8_t* codes, const int (&t)[4], uint4 (&v)[4]) {
+    auto fetch = [&](const uint8_t* codes, const int (&t)[kPer], uint4 (&v)[kPer]) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < kPer; ++i)
         v[i] = t[i] >= 0 && t[i] < s.len
                    ? __ldcg(reinterpret_cast<const uint4*>(codes + (row0 + t[i]) * kDg + pc * 16))
                    : make_uint4(0, 0, 0, 0);
     };
-    int tok[4], tok_next[4], tm = -1, tm_next = -1;  // tm: the key whose scales this thread loads
-    uint4 kv[4], vv[4];
+    int tok[kPer], tok_next[kPer], tm, tm_next;  // tm: the key whose scales this thread loads
+    uint4 kv[kPer], vv[kPer];
     float ks = 0.f, vs = 0.f;
     auto scales = [&]() {
       ks = vs = 0.f;
@@ -185,11 +224,11 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
       }
     };
 #pragma unroll
-    for (int i = 0; i < 4; ++i) tok[i] = token(0, pr + 32 * i);
-    if (pt < kKeysG) tm = token(0, pt);
+    for (int i = 0; i < kPer; ++i) tok[i] = token(0, pr + kRowStep * i);
+    tm = token(0, pt);  // producers are as many as keys
 #pragma unroll
-    for (int i = 0; i < 4; ++i) tok_next[i] = token(1, pr + 32 * i);
-    if (pt < kKeysG) tm_next = token(1, pt);
+    for (int i = 0; i < kPer; ++i) tok_next[i] = token(1, pr + kRowStep * i);
+    tm_next = token(1, pt);
     fetch(a.K, tok, kv);
     scales();
     fetch(a.V, tok, vv);
@@ -201,36 +240,39 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
       }
       const uint32_t kst = sbase + Lay::kStage + st * 2 * kTileG;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) store_codes(kst, pr + 32 * i, pc, kv[i]);
-      if (pt < kKeysG) {
-        if (tm >= s.len) {
-          if (rep) report(a.status, kErrDevice, kKernAttnQ8, (int64_t)b * a.k + e_beg + j * kKeysG + pt, tm, s.len);
-          tm = -1;
-        }
-        meta[st].ks[pt] = ks;
-        const int ex = (int)(__float_as_uint(vs) >> 23 & 0xff);
-        meta[st].vs[pt] = ex == 0 ? 0.f : vs;  // below 2^-126: zero
-        meta[st].ve[pt] = ex == 0 ? 0.f : (float)(ex - 127);
-        const uint32_t seen = __ballot_sync(0xffffffffu, tm >= 0);
-        if (lane == 0) meta[st].seen[pt >> 5] = seen;
+      for (int i = 0; i < kPer; ++i) store_codes(kst, pr + kRowStep * i, pc, kv[i]);
+      if (tm >= s.len) {
+        if (rep) report(a.status, kErrDevice, kKernAttnQ8, (int64_t)b * a.k + e_beg + j * kKeysG + pt, tm, s.len);
+        tm = -1;
+      }
+      meta[st].ks[pt] = ks;
+      const int ex = (int)(__float_as_uint(vs) >> 23 & 0xff);
+      meta[st].vs[pt] = ex == 0 ? 0.f : vs;  // below 2^-126: zero
+      const int ve = max(ex - 127, kMinExp);
+      meta[st].ve[pt] = (float)ve;
+      const uint32_t seen = __ballot_sync(0xffffffffu, tm >= 0);
+      const int top = __reduce_max_sync(0xffffffffu, ve);
+      if (lane == 0) {
+        meta[st].seen[pt >> 5] = seen;
+        meta[st].emax[pt >> 5] = (float)top;
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&k_full[st]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) tok[i] = tok_next[i];
+      for (int i = 0; i < kPer; ++i) tok[i] = tok_next[i];
       tm = tm_next;
       fetch(a.K, tok, kv);
       scales();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) store_codes(kst + kTileG, pr + 32 * i, pc, vv[i]);
+      for (int i = 0; i < kPer; ++i) store_codes(kst + kTileG, pr + kRowStep * i, pc, vv[i]);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&v_full[st]);
       fetch(a.V, tok, vv);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) tok_next[i] = token(j + 2, pr + 32 * i);
-      if (pt < kKeysG) tm_next = token(j + 2, pt);
+      for (int i = 0; i < kPer; ++i) tok_next[i] = token(j + 2, pr + kRowStep * i);
+      tm_next = token(j + 2, pt);
     }
   } else if (warp == kMmaWarp) {
     // =============== MMA issuer ===============
@@ -281,13 +323,18 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
   } else {
     // =============== queries, then softmax ===============
     if (nt > 0) {
-      for (int r = warp; r < kQ8RowTile; r += kSoftWarps) {
-        const int row = row_base + r;
-        uint2 v = make_uint2(0u, 0u);
-        if (row < a.R) {
-          const int64_t off = (((int64_t)(row / a.G) * a.B + b) * a.Hq + g * a.G + row % a.G) * kDg;
-          v = __ldcg(reinterpret_cast<const uint2*>(a.Q + off) + lane);  // dims 4*lane ..
-        }
+      constexpr int kRowsWarp = kQ8RowTile / kSoftWarps;
+      uint2 qv[kRowsWarp];  // rows warp + 8 i, dims 4*lane ..: every load before the first use
+#pragma unroll
+      for (int i = 0; i < kRowsWarp; ++i) {
+        const int row = row_base + warp + kSoftWarps * i;
+        const int64_t off = (((int64_t)(row / a.G) * a.B + b) * a.Hq + g * a.G + row % a.G) * kDg;
+        qv[i] = row < a.R ? __ldcg(reinterpret_cast<const uint2*>(a.Q + off) + lane) : make_uint2(0u, 0u);
+      }
+#pragma unroll
+      for (int i = 0; i < kRowsWarp; ++i) {
+        const int r = warp + kSoftWarps * i;
+        const uint2 v = qv[i];
         const float x0 = bf_lo(v.x), x1 = bf_hi(v.x), x2 = bf_lo(v.y), x3 = bf_hi(v.y);
         const float mx = fmaxf(fmaxf(fabsf(x0), fabsf(x1)), fmaxf(fabsf(x2), fabsf(x3)));
         const uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
@@ -299,7 +346,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
         asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(pack_half2(x0 * up, x1 * up)),
                      "r"(pack_half2(x2 * up, x3 * up))
                      : "memory");
-        if (lane == 0) rf_s[r] = a.scale_log2 / up;
+        if (lane == 0) rf_s[r] = fmaxf(a.scale_log2 / up, 1e-45f);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -325,39 +372,29 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
         const MetaG& mt = meta[st];
         const uint32_t tmem_s = tmem + st * 128 + 64 * half + lane_base;
         const uint32_t vis[2] = {mt.seen[2 * half], mt.seen[2 * half + 1]};
-        // ---- the largest logit, and the largest logit + exponent of its V scale ----
-        float zm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        float ym[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        const uint64_t* ks2 = reinterpret_cast<const uint64_t*>(mt.ks + 64 * half);
+        const uint64_t* vs2 = reinterpret_cast<const uint64_t*>(mt.vs + 64 * half);
+        // ---- the largest logit ----
+        float wm[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) wm[i] = -INFINITY;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t sv[32];
           tmem_ld32(tmem_s + 32 * c, sv);
           tmem_wait_ld();
-          const float4* ks4 = reinterpret_cast<const float4*>(mt.ks + 64 * half + 32 * c);
-          const float4* ve4 = reinterpret_cast<const float4*>(mt.ve + 64 * half + 32 * c);
-          if (vis[c] == 0xffffffffu) {
+          const bool all = vis[c] == 0xffffffffu;
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const float4 k = ks4[q], v = ve4[q];
-              const float z0 = __uint_as_float(sv[4 * q]) * (k.x * rf), z1 = __uint_as_float(sv[4 * q + 1]) * (k.y * rf);
-              const float z2 = __uint_as_float(sv[4 * q + 2]) * (k.z * rf), z3 = __uint_as_float(sv[4 * q + 3]) * (k.w * rf);
-              zm[0] = fmaxf(zm[0], z0), zm[1] = fmaxf(zm[1], z1), zm[2] = fmaxf(zm[2], z2), zm[3] = fmaxf(zm[3], z3);
-              ym[0] = fmaxf(ym[0], z0 + v.x), ym[1] = fmaxf(ym[1], z1 + v.y);
-              ym[2] = fmaxf(ym[2], z2 + v.z), ym[3] = fmaxf(ym[3], z3 + v.w);
-            }
-          } else if (vis[c] != 0u) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (vis[c] >> e & 1u) {
-                const float z = __uint_as_float(sv[e]) * (mt.ks[64 * half + 32 * c + e] * rf);
-                zm[e & 3] = fmaxf(zm[e & 3], z);
-                ym[e & 3] = fmaxf(ym[e & 3], z + mt.ve[64 * half + 32 * c + e]);
-              }
+          for (int q = 0; q < 16; ++q) {
+            const float2 w = unpair(mul2(pair(sv[2 * q], sv[2 * q + 1]), ks2[16 * c + q]));
+            wm[q & 3] = fmaxf(wm[q & 3], all || (vis[c] >> (2 * q) & 1u) ? w.x : -INFINITY);
+            wm[4 + (q & 3)] = fmaxf(wm[4 + (q & 3)], all || (vis[c] >> (2 * q + 1) & 1u) ? w.y : -INFINITY);
           }
         }
-        const float zmax = fmaxf(fmaxf(zm[0], zm[1]), fmaxf(zm[2], zm[3]));
-        const float ymax = fmaxf(fmaxf(ym[0], ym[1]), fmaxf(ym[2], ym[3]));
+        const float zmax = rf * fmaxf(fmaxf(fmaxf(wm[0], wm[1]), fmaxf(wm[2], wm[3])),
+                                      fmaxf(fmaxf(wm[4], wm[5]), fmaxf(wm[6], wm[7])));
         float alpha = 1.f;
+        bool look = false;  // whether P may leave its range: then the largest weight decides
         if (zmax > m + 14.f) {  // also when the row has no reference yet
           const float to = ceilf(zmax);
           if (m == -INFINITY) {
@@ -368,28 +405,45 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
           }
           m = to;
         }
-        if (ymax - m + lc > 14.f || lc > 126.f) {
-          const float to = fmaxf(fminf(fminf(lc, m - ceilf(ymax) + 7.f), 126.f), -126.f);
-          alpha = ex2f(fminf(to - lc, 126.f));
-          lc = to;
-        }
-        if (__any_sync(0xffffffffu, alpha != 1.f) && j > 0) {
-          // the last tile's PV must have landed before O is rescaled
-          if (!warp_wait_g(&o_done[(j - 1) & 3], ((j - 1) >> 2) & 1)) {
-            failed = true;
-            break;
-          }
-          tc_fence_after();
+        look = zmax > -INFINITY && (zmax - m + fmaxf(mt.emax[2 * half], mt.emax[2 * half + 1]) + lc > 14.f || lc > kMaxLc);
+        if (__any_sync(0xffffffffu, look)) {
+          float ymax = -INFINITY;  // the largest logit + exponent of its V scale
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
-            uint32_t ov[32];
-            tmem_ld32(tmem_o + c * 32, ov);
+            uint32_t sv[16];
+            tmem_ld16(tmem_s + 16 * c, sv);
             tmem_wait_ld();
+            const uint32_t see = vis[c >> 1] >> (16 * (c & 1));
 #pragma unroll
-            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-            tmem_st32(tmem_o + c * 32, ov);
+            for (int e = 0; e < 16; ++e) {
+              const int at = 64 * half + 16 * c + e;
+              const float y = fmaf(__uint_as_float(sv[e]) * mt.ks[at], rf, mt.ve[at]);
+              if (see >> e & 1u) ymax = fmaxf(ymax, y);
+            }
           }
-          tmem_wait_st();
+          if (look && (ymax - m + lc > 14.f || lc > kMaxLc)) {
+            const float to = fmaxf(fminf(fminf(lc, m - ceilf(ymax) + 7.f), kMaxLc), -126.f);
+            alpha = ex2f(to - lc);
+            lc = to;
+          }
+          if (__any_sync(0xffffffffu, alpha != 1.f) && j > 0) {
+            // the last tile's PV must have landed before O is rescaled
+            if (!warp_wait_g(&o_done[(j - 1) & 3], ((j - 1) >> 2) & 1)) {
+              failed = true;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint32_t ov[16];
+              tmem_ld16(tmem_o + c * 16, ov);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+              tmem_st16(tmem_o + c * 16, ov);
+            }
+            tmem_wait_st();
+          }
         }
         // ---- P over this half of the consumed K tile ----
         if (PRECISE && j > 0 && !warp_wait_g(&o_done[(j - 1) & 3], ((j - 1) >> 2) & 1)) {
@@ -398,8 +452,9 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
         }
         const float neg_m = m == -INFINITY ? 0.f : -m;
         const float unit_c = __int_as_float(((int)lc + 127) << 23);  // 2^lc
+        const uint64_t rf2 = pair(rf, rf), neg2 = pair(neg_m, neg_m), unit2 = pair(unit_c, unit_c);
         const uint32_t pst = sbase + Lay::kStage + st * 2 * kTileG + half * kHalfG;
-        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+        uint64_t ls[2] = {0ull, 0ull};
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t sv[32];
@@ -407,39 +462,38 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
           tmem_wait_ld();
           const bool all = vis[c] == 0xffffffffu;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            float p[8];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int at = 64 * half + 32 * c + 8 * q + 4 * u;
-              const float4 k = *reinterpret_cast<const float4*>(mt.ks + at);
-              const float4 v = *reinterpret_cast<const float4*>(mt.vs + at);
-              const float kk[4] = {k.x, k.y, k.z, k.w}, vv[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int col = 8 * q + 4 * u + e;
-                float x = ex2f(fmaf(__uint_as_float(sv[col]), kk[e] * rf, neg_m));
-                if (!all && !(vis[c] >> col & 1u)) x = 0.f;
-                ls[e] += x;
-                p[4 * u + e] = x * fminf(vv[e] * unit_c, 0x1p126f);
-              }
-            }
-            const uint32_t off = sw128_offset(r_loc, 4 * c + q);
+          for (int q = 0; q < 4; ++q) {  // 8 keys: one 16-byte chunk of the row's P
+            uint64_t pv[4];
             uint32_t h[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) h[i] = pack_half2(p[2 * i], p[2 * i + 1]);
+            for (int i = 0; i < 4; ++i) {
+              const int at = 4 * q + i;
+              const float2 x = unpair(fma2(mul2(pair(sv[2 * at], sv[2 * at + 1]), ks2[16 * c + at]), rf2, neg2));
+              float2 y = make_float2(ex2f(x.x), ex2f(x.y));
+              if (!all) {
+                y.x = vis[c] >> (2 * at) & 1u ? y.x : 0.f;
+                y.y = vis[c] >> (2 * at + 1) & 1u ? y.y : 0.f;
+              }
+              const uint64_t y2 = pair(y.x, y.y);
+              ls[i & 1] = add2(ls[i & 1], y2);
+              pv[i] = mul2(y2, mul2(vs2[16 * c + at], unit2));
+              const float2 f = unpair(pv[i]);
+              h[i] = pack_half2(f.x, f.y);
+            }
+            const uint32_t off = sw128_offset(r_loc, 4 * c + q);
             sts16(pst + off, h[0], h[1], h[2], h[3]);
             if (PRECISE) {
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-                h[i] = pack_half2(p[2 * i] - f.x, p[2 * i + 1] - f.y);
+                const float2 f = unpair(pv[i]), t = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+                h[i] = pack_half2(f.x - t.x, f.y - t.y);
               }
               sts16(sbase + Lay::kPlo + half * kHalfG + off, h[0], h[1], h[2], h[3]);
             }
           }
         }
-        l_run += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        const float2 l0 = unpair(ls[0]), l1 = unpair(ls[1]);
+        l_run += (l0.x + l0.y) + (l1.x + l1.y);
         fence_proxy_async_smem();
       }
       tc_fence_before();
@@ -449,32 +503,45 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
         mbar_arrive(&p_full[st]);
       }
     }
-    // ---- this slice's (m, l, o / l) of the row and key half ----
+    // ---- the row's two key halves into one (m, l, o / l) in shared memory ----
     if (nt > 0 && !failed) failed = !warp_wait_g(&o_done[(nt - 1) & 3], ((nt - 1) >> 2) & 1);
-    if (failed) {
-      if (lane == 0) report(a.status, kErrTimeout, kKernAttnQ8, blockIdx.x, 2, warp);
-    } else if (active) {
-      const int64_t at = (part0 + half) * kQ8RowTile + r_loc;
-      if (row_base + r_loc < a.R) __stcg(&a.pml[at], make_float2(m, l_run));
-      if (nt > 0) {
-        tc_fence_after();
-        const float inv = l_run == 0.f ? 0.f : 1.f / l_run;  // a NaN sum stays one
-        const float f = inv * __int_as_float((127 - (int)lc) << 23);  // o's unit is 2^lc
-        float* dst = a.po + at * kDg;
+    if (failed && lane == 0) report(a.status, kErrTimeout, kKernAttnQ8, blockIdx.x, 2, warp);
+    tc_fence_after();
+    // every MMA is done (the barrier): the stages are free for the rows
+    float2* ml_s = reinterpret_cast<float2*>(smem + Lay::kMeta);  // [2][128]
+    float* o_s = reinterpret_cast<float*>(smem + Lay::kStage);
+    ml_s[half * kQ8RowTile + r_loc] = make_float2(m, l_run);
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    const float2 other = ml_s[(half ^ 1) * kQ8RowTile + r_loc];
+    const float M = fmaxf(m, other.x);
+    const float mine = m == -INFINITY ? l_run : ex2f(m - M);  // an empty half: 0, or a NaN sum
+    const float L = mine * l_run + (other.x == -INFINITY ? other.y : ex2f(other.x - M) * other.y);
+    // o's unit is 2^lc
+    const float f = (L == 0.f ? 0.f : mine / L) * __int_as_float((127 - (int)fmaxf(lc, -126.f)) << 23);
+    auto rows = [&](bool add) {
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t ov[32];
-          tmem_ld32(tmem_o + c * 32, ov);
-          tmem_wait_ld();
-          if (row_base + r_loc < a.R) {
+      for (int c = 0; c < 4; ++c) {
+        uint32_t ov[32];
+        tmem_ld32(tmem_o + c * 32, ov);
+        tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              __stcg(reinterpret_cast<float4*>(dst + c * 32 + e),
-                     make_float4(__uint_as_float(ov[e]) * f, __uint_as_float(ov[e + 1]) * f,
-                                 __uint_as_float(ov[e + 2]) * f, __uint_as_float(ov[e + 3]) * f));
+        for (int e = 0; e < 32; e += 4) {
+          float4* at = reinterpret_cast<float4*>(o_s + r_loc * kORowG + c * 32 + e);
+          float4 v = make_float4(__uint_as_float(ov[e]) * f, __uint_as_float(ov[e + 1]) * f,
+                                 __uint_as_float(ov[e + 2]) * f, __uint_as_float(ov[e + 3]) * f);
+          if (add) {
+            const float4 t = *at;
+            v.x += t.x, v.y += t.y, v.z += t.z, v.w += t.w;
           }
+          *at = v;
         }
       }
+    };
+    if (half == 1 && active && nt > 0) rows(false);
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    if (half == 0 && active) {
+      if (nt > 0) rows(true);
+      if (row_base + r_loc < a.R) __stcg(&a.pml[part * kQ8RowTile + r_loc], make_float2(M, L));
     }
   }
   tc_fence_before();
@@ -482,6 +549,13 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+  }
+  if (nt > 0) {
+    const float* o_s = reinterpret_cast<const float*>(smem + Lay::kStage);
+    const int n = min(kQ8RowTile, a.R - row_base) * (kDg / 4);
+    float4* dst = reinterpret_cast<float4*>(a.po + part * kQ8RowTile * kDg);
+    for (int i = tid; i < n; i += kThreadsG)
+      __stcg(dst + i, *reinterpret_cast<const float4*>(o_s + i / (kDg / 4) * kORowG + i % (kDg / 4) * 4));
   }
 }
 
@@ -494,7 +568,7 @@ __global__ void __launch_bounds__(256) attn_q8_merge_kernel(const Q8AttnArgs a, 
   if (i >= n_rows) return;
   const int row = i % a.R, bg = i / a.R;
   const int g = bg % a.Hkv, b = bg / a.Hkv;
-  const int n = 2 * a.n_split;
+  const int n = a.n_split;
   const int64_t p0 = ((int64_t)bg * row_tiles + row / kQ8RowTile) * n * kQ8RowTile + row % kQ8RowTile;
   float M = -INFINITY;
   for (int p = lane; p < n; p += 32) M = fmaxf(M, __ldcg(&a.pml[p0 + (int64_t)p * kQ8RowTile]).x);
@@ -552,7 +626,7 @@ void plan_attn_q8_group(Q8AttnPlan& p, int64_t n, int sms) {
   if (split > tiles) split = tiles;
   p.chunk = (int)((tiles + split - 1) / split) * kKeysG;
   p.n_split = (int)((tiles * kKeysG + p.chunk - 1) / p.chunk);
-  p.parts = 2 * p.n_split;
+  p.parts = p.n_split;
   p.rows = kQ8RowTile;
 }
 
