@@ -11,22 +11,22 @@
 //
 //   * Warps 9-12 (producers) load the codes of a tile straight into registers
 //     (16 bytes a lane, the next K and V pieces in flight while the last ones
-//     are stored), make halves of them (exact) and write them as 128-byte
-//     swizzled tiles, K as [keys, d] K-major, V the same rows read MN-major.
+//     are stored) and write scale * code as bf16: exact for the powers of two
+//     an append writes (4 significant bits), so S and PV see the cache's own
+//     values and the softmax no scales.  K as [keys, d] K-major, V the same
+//     rows read MN-major, 128-byte swizzled.
 //   * Warp 8 issues S = Q K^T and, per key half h, O_h += P_h V_h.
 //   * Warps 0-7: softmax, one query row per thread and key half, P written
-//     over the consumed K tile.  The V scale joins P, not V: with l the sum of
-//     p = 2^(z - m), O sums p * (vs 2^lc).  m and lc are whole numbers, m moves
-//     when a logit passes it by 14 and lc keeps the largest p vs 2^lc between
-//     2^7 and 2^14: halves hold a weight's 11 bits, however far the scales are
-//     apart, and moving m costs no pass over O (lc takes it up).  (lc stops at
-//     67: V scales below 2^-60 lose their weights' bits towards f16's
-//     subnormals.)  fp32 outputs use two halves per weight (22 bits).
-//   * Queries enter as halves scaled per row by a power of two (as in
-//     attn_q8.cu); each row leaves its slice's (m, l, o / l) in the workspace,
-//     and a second kernel merges them.  It is launched with
-//     programmatic dependence and reads one row per warp, so the merge uses
-//     the whole GPU and no counters.
+//     over the consumed K tile.  One pass: weights are 2^(z - m) with m the
+//     row's first logit until one passes it by 30 (fp32 and bf16 have the
+//     exponents for that); only then the row's sums move to a new m and the
+//     tile's weights are made again.
+//   * bf16 outputs: weights are rounded to bf16, 8 bits, and l is the sum of
+//     the rounded ones, so that they add up to one.  fp32 outputs: three bf16
+//     parts (24 bits), for whose shared memory K has one stage instead of two.
+//   * Each row leaves its slice's (m, l, o / l) in the workspace, and a second
+//     kernel merges them.  It is launched with programmatic dependence and
+//     reads one row per warp, so the merge uses the whole GPU and no counters.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -46,53 +46,37 @@ constexpr int kKeysG = 128;     // keys of a tile
 constexpr int kSoftWarps = 8, kMmaWarp = 8, kProdWarp = 9, kProdWarps = 4;
 constexpr int kThreadsG = 32 * (kProdWarp + kProdWarps);
 constexpr int kPer = 128 * 8 / (32 * kProdWarps);  // 16-byte pieces of a K (or V) tile a producer holds
-static_assert(32 * kProdWarps == kKeysG, "one producer thread per key's scales");
 constexpr int kRowStep = 128 / kPer;
+static_assert(32 * kProdWarps == kKeysG, "one producer thread per key's token and scales");
 constexpr int kHalfG = 16384;   // 128 rows x 128 bytes
 constexpr int kTileG = 2 * kHalfG;
-constexpr int kStagesG = 2;
+constexpr float kRangeG = 30.f;  // log2 units a logit may pass its row's m by
 constexpr int kORowG = kDg + 4;  // floats of an output row in shared memory
-
-constexpr int kMinExp = -60;
-constexpr float kMaxLc = 7.f - kMinExp;
-
-struct alignas(16) MetaG {
-  float ks[kKeysG], vs[kKeysG], ve[kKeysG];  // scales, and the exponent of vs (at least kMinExp)
-  uint32_t seen[4];                          // bit c of word w: key 32w + c is a token
-  float emax[4];                             // largest ve of the word
-};
 
 template <bool PRECISE>
 struct SmemG {
-  static constexpr int kStage = kTileG;                           // after Q: K then V of each stage
-  static constexpr int kPlo = kStage + kStagesG * 2 * kTileG;     // low halves of P
-  static constexpr int kMeta = kPlo + (PRECISE ? kTileG : 0);
-  static constexpr int kRf = kMeta + kStagesG * (int)sizeof(MetaG);
-  static constexpr int kBar = kRf + kQ8RowTile * 4;
-  // k_full[2] v_full[2] kv_empty[2] s_full[2] s_free[2] p_full[2] o_done[4] q_full
-  static constexpr int kSlot = kBar + 8 * 17;
+  static constexpr int kStagesK = PRECISE ? 1 : 2, kStagesV = 2;
+  static constexpr int kParts = PRECISE ? 3 : 1;         // of P: the first over the K tile
+  static constexpr int kK = kTileG;                      // after Q
+  static constexpr int kV = kK + kStagesK * kTileG;
+  static constexpr int kPlo = kV + kStagesV * kTileG;
+  static constexpr int kTok = kPlo + (kParts - 1) * kTileG;  // [2][128]: tokens of a tile's keys, -1 for none
+  static constexpr int kScale = kTok + 2 * kKeysG * 4;       // [2][128]: their (K, V) scales
+  static constexpr int kSeen = kScale + 2 * kKeysG * 8;      // [2][4]: bit c of word w: key 32w + c is a token
+  static constexpr int kMl = kSeen + 2 * 4 * 4;              // [2][128]: (m, l) of the rows' key halves
+  // k_full[2] v_full[2] k_empty[2] v_empty[2] s_full[2] s_free[2] p_full[2] o_done[4] q_full
+  static constexpr int kBar = kMl + 2 * kQ8RowTile * 8;
+  static constexpr int kSlot = kBar + 8 * 19;
   static constexpr size_t kBytes = 1024 + kSlot + 16;
   static_assert(kBytes <= 232448, "shared memory budget");
+  static_assert(2 * kQ8RowTile * kORowG * 4 <= kTok, "the output rows fit over Q and the stages");
 };
-
-__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
-  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 
 // two floats at once
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
   return r;
-}
-__device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
-  return pair(__uint_as_float(lo), __uint_as_float(hi));
 }
 __device__ __forceinline__ float2 unpair(uint64_t v) {
   float2 r;
@@ -115,8 +99,10 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
+// Operand tiles are only ever read by the MMAs, behind a fence: no "memory"
+// clobber, so that other shared-memory loads may pass these stores.
 __device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d));
 }
 
 __device__ __forceinline__ bool warp_wait_g(uint64_t* bar, uint32_t parity) {
@@ -125,34 +111,41 @@ __device__ __forceinline__ bool warp_wait_g(uint64_t* bar, uint32_t parity) {
   return __shfl_sync(0xffffffffu, ok, 0);
 }
 
-// 16 codes (dims 16c ..) of key row r as halves into a [128, 128] tile at `tile`.
-// A half row is 64 dims; the two 16-byte chunks are stored in the order that
-// keeps the 8 lanes of a row on different banks.
-__device__ __forceinline__ void store_codes(uint32_t tile, int r, int c, const uint4& v) {
-  uint32_t h[8];
-  q8_to_half4(v.x, h[0], h[1]);
-  q8_to_half4(v.y, h[2], h[3]);
-  q8_to_half4(v.z, h[4], h[5]);
-  q8_to_half4(v.w, h[6], h[7]);
-  const int up = c >> 2;
-  const uint32_t base = tile + up * kHalfG;
-  const uint32_t a0 = base + sw128_offset(r, (c & 3) * 2), a1 = base + sw128_offset(r, (c & 3) * 2 + 1);
-  sts16(up ? a1 : a0, up ? h[4] : h[0], up ? h[5] : h[1], up ? h[6] : h[2], up ? h[7] : h[3]);
-  sts16(up ? a0 : a1, up ? h[0] : h[4], up ? h[1] : h[5], up ? h[2] : h[6], up ? h[3] : h[7]);
+// 16 codes (dims 16c ..) of key row r times their scale as bf16 into a
+// [128, 128] tile at `tile` (a half row is 64 dims).  The 8 lanes of a store
+// phase hold pieces 0-3 of one row and 4-7 of its neighbour: different banks.
+__device__ __forceinline__ void store_codes(uint32_t tile, int r, int c, const uint4& v, float scale) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const uint64_t sc = pair(scale, scale);
+  uint32_t b[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t lo, hi;
+    q8_to_half4(w[i], lo, hi);
+    const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+    const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    const float2 g0 = unpair(mul2(pair(f0.x, f0.y), sc)), g1 = unpair(mul2(pair(f1.x, f1.y), sc));
+    b[2 * i] = pack_bf16(g0.x, g0.y);
+    b[2 * i + 1] = pack_bf16(g1.x, g1.y);
+  }
+  const uint32_t base = tile + (c >> 2) * kHalfG;
+  sts16(base + sw128_offset(r, (c & 3) * 2), b[0], b[1], b[2], b[3]);
+  sts16(base + sw128_offset(r, (c & 3) * 2 + 1), b[4], b[5], b[6], b[7]);
 }
 
 template <bool PRECISE>
 __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8AttnArgs a, const int row_tiles) {
   using Lay = SmemG<PRECISE>;
+  constexpr int SK = Lay::kStagesK, SV = Lay::kStagesV;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
-  MetaG* meta = reinterpret_cast<MetaG*>(smem + Lay::kMeta);
-  float* rf_s = reinterpret_cast<float*>(smem + Lay::kRf);
+  uint32_t* seen_s = reinterpret_cast<uint32_t*>(smem + Lay::kSeen);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + Lay::kBar);
   uint64_t* v_full = k_full + 2;
-  uint64_t* kv_empty = v_full + 2;
-  uint64_t* s_full = kv_empty + 2;
+  uint64_t* k_empty = v_full + 2;
+  uint64_t* v_empty = k_empty + 2;
+  uint64_t* s_full = v_empty + 2;
   uint64_t* s_free = s_full + 2;
   uint64_t* p_full = s_free + 2;
   uint64_t* o_done = p_full + 2;  // [4]: PV of tile i on o_done[i % 4]
@@ -164,6 +157,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
   const int rt = unit % row_tiles;
   const int g = unit / row_tiles % a.Hkv, b = unit / row_tiles / a.Hkv;
   const int row_base = rt * kQ8RowTile;
+  const int64_t part = (int64_t)unit * a.n_split + slice;
 
   pdl_trigger();
   if (warp == kMmaWarp) {
@@ -172,7 +166,8 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
       for (int i = 0; i < 2; ++i) {
         mbar_init(&k_full[i], kProdWarps);
         mbar_init(&v_full[i], kProdWarps);
-        mbar_init(&kv_empty[i], 1);
+        mbar_init(&k_empty[i], 1);
+        mbar_init(&v_empty[i], 1);
         mbar_init(&s_full[i], 1);
         mbar_init(&s_free[i], kSoftWarps);
         mbar_init(&p_full[i], kSoftWarps);
@@ -186,136 +181,135 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
   const Q8Seq s = q8_seq(a.seq_off, a.seq_len, b, a.n_tokens, a.S_max);
   if (!s.ok && tid == 0 && slice == 0) report(a.status, kErrDevice, kKernAttnQ8, b, s.len, s.cap);
   const int n_keys = !s.ok ? 0 : a.idx ? a.k : s.len;  // entries, or tokens
-  const int e_beg = min(n_keys, slice * a.chunk), e_end = min(n_keys, e_beg + a.chunk);
+  const int e_beg = (int)min((int64_t)n_keys, (int64_t)slice * a.chunk), e_end = min(n_keys, e_beg + a.chunk);
   const int nt = (e_end - e_beg + kKeysG - 1) / kKeysG;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *slot;
-  const int64_t part = (int64_t)unit * a.n_split + slice;
 
   if (warp >= kProdWarp) {
     // =============== producers ===============
     const int pt = tid - kProdWarp * 32;
-    const int pr = pt >> 3, pc = pt & 7;  // rows pr + kRowStep i, 16-byte piece pc
+    const int pc = pt & 7, pr = (pt >> 3) ^ (pc >> 2);  // rows pr + kRowStep i, 16-byte piece pc
     const int64_t row0 = s.off * a.Hkv + (int64_t)g * s.cap;
-    const bool rep = g == 0 && rt == 0;
-    // token of key r of tile j, or -1
-    auto token = [&](int j, int r) -> int {
-      const int e = e_beg + j * kKeysG + r;
+    int* tok_s = reinterpret_cast<int*>(smem + Lay::kTok);
+    float2* scale_s = reinterpret_cast<float2*>(smem + Lay::kScale);
+    // this thread's key of tile j: its token as listed (it loads the key's scales too)
+    auto token = [&](int j) -> int {
+      const int e = e_beg + j * kKeysG + pt;
       if (e >= e_end) return -1;
       return a.idx ? __ldcg(&a.idx[(int64_t)b * a.k + e]) : e;
     };
-    auto fetch = [&](const uint8_t* codes, const int (&t)[kPer], uint4 (&v)[kPer]) {
+    auto sync = [] { asm volatile("bar.sync 2, %0;" ::"n"(32 * kProdWarps) : "memory"); };
+    auto fetch = [&](const uint8_t* codes, int j, uint4 (&v)[kPer]) {
+      const uint8_t* from = codes + row0 * kDg + pc * 16;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        v[i] = t[i] >= 0 && t[i] < s.len
-                   ? __ldcg(reinterpret_cast<const uint4*>(codes + (row0 + t[i]) * kDg + pc * 16))
-                   : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < kPer; ++i) {
+        const int t = tok_s[(j & 1) * kKeysG + pr + kRowStep * i];
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (t >= 0) v[i] = __ldcg(reinterpret_cast<const uint4*>(from + (int64_t)t * kDg));
+      }
     };
-    int tok[kPer], tok_next[kPer], tm, tm_next;  // tm: the key whose scales this thread loads
     uint4 kv[kPer], vv[kPer];
     float ks = 0.f, vs = 0.f;
-    auto scales = [&]() {
+    auto scales = [&](int t) {
       ks = vs = 0.f;
-      if (tm >= 0 && tm < s.len) {
-        ks = __ldcg(a.Ks + (row0 + tm) / kQ8Block);
-        vs = __ldcg(a.Vs + (row0 + tm) / kQ8Block);
+      if (t >= 0 && t < s.len) {
+        ks = __ldcg(a.Ks + (row0 + t) / kQ8Block);
+        vs = __ldcg(a.Vs + (row0 + t) / kQ8Block);
       }
     };
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) tok[i] = token(0, pr + kRowStep * i);
-    tm = token(0, pt);  // producers are as many as keys
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) tok_next[i] = token(1, pr + kRowStep * i);
-    tm_next = token(1, pt);
-    fetch(a.K, tok, kv);
-    scales();
-    fetch(a.V, tok, vv);
+    int tm = token(0), tm_next = token(1);
+    tok_s[pt] = tm < s.len ? tm : -1;
+    sync();
+    fetch(a.K, 0, kv);
+    scales(tm);
+    fetch(a.V, 0, vv);
+    bool dead = false;
     for (int j = 0; j < nt; ++j) {
-      const int st = j & 1;
-      if (j >= kStagesG && !warp_wait_g(&kv_empty[st], ((j >> 1) & 1) ^ 1)) {
-        if (lane == 0) report(a.status, kErrTimeout, kKernAttnQ8, blockIdx.x, 0, j);
-        break;
-      }
-      const uint32_t kst = sbase + Lay::kStage + st * 2 * kTileG;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) store_codes(kst, pr + kRowStep * i, pc, kv[i]);
+      const int sk = j % SK, sv = j % SV;
       if (tm >= s.len) {
-        if (rep) report(a.status, kErrDevice, kKernAttnQ8, (int64_t)b * a.k + e_beg + j * kKeysG + pt, tm, s.len);
+        if (g == 0 && rt == 0)
+          report(a.status, kErrDevice, kKernAttnQ8, (int64_t)b * a.k + e_beg + j * kKeysG + pt, tm, s.len);
         tm = -1;
       }
-      meta[st].ks[pt] = ks;
-      const int ex = (int)(__float_as_uint(vs) >> 23 & 0xff);
-      meta[st].vs[pt] = ex == 0 ? 0.f : vs;  // below 2^-126: zero
-      const int ve = max(ex - 127, kMinExp);
-      meta[st].ve[pt] = (float)ve;
+      scale_s[(j & 1) * kKeysG + pt] = make_float2(ks, vs);
       const uint32_t seen = __ballot_sync(0xffffffffu, tm >= 0);
-      const int top = __reduce_max_sync(0xffffffffu, ve);
-      if (lane == 0) {
-        meta[st].seen[pt >> 5] = seen;
-        meta[st].emax[pt >> 5] = (float)top;
+      if (!dead && ((j >= SK && !warp_wait_g(&k_empty[sk], (j / SK - 1) & 1)) ||
+                    (j >= SV && !warp_wait_g(&v_empty[sv], (j / SV - 1) & 1)))) {
+        if (lane == 0) report(a.status, kErrTimeout, kKernAttnQ8, blockIdx.x, 0, j);
+        dead = true;  // only meets the other producers from here on
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&k_full[st]);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) tok[i] = tok_next[i];
+      if (lane == 0 && !dead) seen_s[(j & 1) * 4 + (pt >> 5)] = seen;
       tm = tm_next;
-      fetch(a.K, tok, kv);
-      scales();
+      const int t = tm < s.len ? tm : -1;
+      tok_s[((j + 1) & 1) * kKeysG + pt] = t;
+      sync();
+      if (dead) continue;
+      const float2* sc = scale_s + (j & 1) * kKeysG + pr;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) store_codes(kst + kTileG, pr + kRowStep * i, pc, vv[i]);
+      for (int i = 0; i < kPer; ++i)
+        store_codes(sbase + Lay::kK + sk * kTileG, pr + kRowStep * i, pc, kv[i], sc[kRowStep * i].x);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&v_full[st]);
-      fetch(a.V, tok, vv);
+      if (lane == 0) mbar_arrive(&k_full[sk]);
+      fetch(a.K, j + 1, kv);
+      scales(tm);
+      tm_next = token(j + 2);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) tok_next[i] = token(j + 2, pr + kRowStep * i);
-      tm_next = token(j + 2, pt);
+      for (int i = 0; i < kPer; ++i)
+        store_codes(sbase + Lay::kV + sv * kTileG, pr + kRowStep * i, pc, vv[i], sc[kRowStep * i].y);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&v_full[sv]);
+      fetch(a.V, j + 1, vv);
     }
   } else if (warp == kMmaWarp) {
     // =============== MMA issuer ===============
     if (lane == 0 && nt > 0) {
-      constexpr uint32_t idesc_qk = idesc_f16(128, 128, false), idesc_pv = idesc_f16(128, 128, true);
+      constexpr uint32_t idesc_qk = umma_idesc_bf16(128, 128, false, false);
+      constexpr uint32_t idesc_pv = umma_idesc_bf16(128, 128, false, true);
       auto pv = [&](int i) -> bool {
-        const int st = i & 1;
-        if (!mbar_wait(&v_full[st], (i >> 1) & 1, kWaitLimitNs) || !mbar_wait(&p_full[st], (i >> 1) & 1, kWaitLimitNs))
+        if (!mbar_wait(&v_full[i % SV], (i / SV) & 1, kWaitLimitNs) ||
+            !mbar_wait(&p_full[i & 1], (i >> 1) & 1, kWaitLimitNs))
           return false;
         tc_fence_after();
-        const uint32_t kst = sbase + Lay::kStage + st * 2 * kTileG;  // P lives here now
-        const uint32_t vst = kst + kTileG;
+        const uint32_t pst = sbase + Lay::kK + i % SK * kTileG;  // P lives here now
+        const uint32_t vst = sbase + Lay::kV + i % SV * kTileG;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {  // keys 64h + 16kk ..
             const uint64_t vd = umma_desc_sw128(vst + h * 8192 + kk * 2048, kHalfG, 1024);
-            umma_bf16(tmem + 256 + 128 * h, umma_desc_sw128(kst + h * kHalfG + kk * 32, 16, 1024), vd, idesc_pv,
-                      (i | kk) != 0);
-            if (PRECISE)
-              umma_bf16(tmem + 256 + 128 * h, umma_desc_sw128(sbase + Lay::kPlo + h * kHalfG + kk * 32, 16, 1024), vd,
-                        idesc_pv, 1);
+#pragma unroll
+            for (int q = 0; q < Lay::kParts; ++q)
+              umma_bf16(tmem + 256 + 128 * h,
+                        umma_desc_sw128((q == 0 ? pst : sbase + Lay::kPlo + (q - 1) * kTileG) + h * kHalfG + kk * 32, 16,
+                                        1024),
+                        vd, idesc_pv, (i | kk | q) != 0);
           }
-        umma_commit(&kv_empty[st]);
+        umma_commit(&k_empty[i % SK]);
+        umma_commit(&v_empty[i % SV]);
         umma_commit(&o_done[i & 3]);
         return true;
       };
       bool ok = mbar_wait(q_full, 0, kWaitLimitNs);
       for (int j = 0; j < nt && ok; ++j) {
-        const int st = j & 1;
-        ok = mbar_wait(&k_full[st], (j >> 1) & 1, kWaitLimitNs) &&
-             mbar_wait(&s_free[st], ((j >> 1) & 1) ^ 1, kWaitLimitNs);
+        if (PRECISE && j >= 1 && !(ok = pv(j - 1))) break;  // the next K tile follows it
+        ok = mbar_wait(&k_full[j % SK], (j / SK) & 1, kWaitLimitNs) &&
+             mbar_wait(&s_free[j & 1], ((j >> 1) & 1) ^ 1, kWaitLimitNs);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t kst = sbase + Lay::kStage + st * 2 * kTileG;
+        const uint32_t kst = sbase + Lay::kK + j % SK * kTileG;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma_bf16(tmem + st * 128, umma_desc_sw128(sbase + h * kHalfG + kk * 32, 16, 1024),
+            umma_bf16(tmem + (j & 1) * 128, umma_desc_sw128(sbase + h * kHalfG + kk * 32, 16, 1024),
                       umma_desc_sw128(kst + h * kHalfG + kk * 32, 16, 1024), idesc_qk, (h | kk) != 0);
-        umma_commit(&s_full[st]);
-        if (j >= 1) ok = pv(j - 1);
+        umma_commit(&s_full[j & 1]);
+        if (!PRECISE && j >= 1) ok = pv(j - 1);
       }
       if (ok) ok = pv(nt - 1);
       if (!ok) report(a.status, kErrTimeout, kKernAttnQ8, blockIdx.x, 1, 0);
@@ -323,31 +317,19 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
   } else {
     // =============== queries, then softmax ===============
     if (nt > 0) {
-      constexpr int kRowsWarp = kQ8RowTile / kSoftWarps;
-      uint2 qv[kRowsWarp];  // rows warp + 8 i, dims 4*lane ..: every load before the first use
+      const int r = tid >> 1, qh = tid & 1;  // half a query row: dims 64 qh ..
+      const int row = row_base + r;
+      uint4 qv[8];
 #pragma unroll
-      for (int i = 0; i < kRowsWarp; ++i) {
-        const int row = row_base + warp + kSoftWarps * i;
-        const int64_t off = (((int64_t)(row / a.G) * a.B + b) * a.Hq + g * a.G + row % a.G) * kDg;
-        qv[i] = row < a.R ? __ldcg(reinterpret_cast<const uint2*>(a.Q + off) + lane) : make_uint2(0u, 0u);
+      for (int i = 0; i < 8; ++i) qv[i] = make_uint4(0, 0, 0, 0);
+      if (row < a.R) {
+        const int64_t off = (((int64_t)(row / a.G) * a.B + b) * a.Hq + g * a.G + row % a.G) * kDg + 64 * qh;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) qv[i] = __ldcg(reinterpret_cast<const uint4*>(a.Q + off) + i);
       }
 #pragma unroll
-      for (int i = 0; i < kRowsWarp; ++i) {
-        const int r = warp + kSoftWarps * i;
-        const uint2 v = qv[i];
-        const float x0 = bf_lo(v.x), x1 = bf_hi(v.x), x2 = bf_lo(v.y), x3 = bf_hi(v.y);
-        const float mx = fmaxf(fmaxf(fabsf(x0), fabsf(x1)), fmaxf(fabsf(x2), fabsf(x3)));
-        const uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
-        // 2^e with the largest element in [2^14, 2^15); 1 for zero or non-finite rows
-        int e = mb == 0u || mb >= 0x7f800000u ? 127 : 127 + 14 + 127 - (int)(mb >> 23);
-        e = min(e, 253);  // tiny rows: as large as a float scale goes
-        const float up = __uint_as_float((uint32_t)e << 23);
-        const uint32_t at = sbase + (lane >> 4) * kHalfG + sw128_offset(r, (lane & 15) >> 1) + (lane & 1) * 8;
-        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(pack_half2(x0 * up, x1 * up)),
-                     "r"(pack_half2(x2 * up, x3 * up))
-                     : "memory");
-        if (lane == 0) rf_s[r] = fmaxf(a.scale_log2 / up, 1e-45f);
-      }
+      for (int i = 0; i < 8; ++i)
+        sts16(sbase + qh * kHalfG + sw128_offset(r, i), qv[i].x, qv[i].y, qv[i].z, qv[i].w);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
@@ -357,81 +339,86 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
     const bool active = row_base + (warp & 3) * 32 < a.R;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tmem_o = tmem + 256 + 128 * half + lane_base;
-    float m = -INFINITY, lc = 0.f, l_run = 0.f, rf = 0.f;
+    const uint64_t scale2 = pair(a.scale_log2, a.scale_log2);
+    float m = -INFINITY, l_run = 0.f;
     bool failed = false;
     for (int j = 0; j < nt; ++j) {
-      const int st = j & 1;
-      if (!warp_wait_g(&s_full[st], (j >> 1) & 1) || !warp_wait_g(&k_full[st], (j >> 1) & 1) ||
-          (j == 0 && !warp_wait_g(q_full, 0))) {
+      if (!warp_wait_g(&s_full[j & 1], (j >> 1) & 1) || !warp_wait_g(&k_full[j % SK], (j / SK) & 1)) {
         failed = true;
         break;
       }
       tc_fence_after();
+      const uint32_t* vis = seen_s + (j & 1) * 4 + 2 * half;
       if (active) {
-        if (j == 0) rf = rf_s[r_loc];
-        const MetaG& mt = meta[st];
-        const uint32_t tmem_s = tmem + st * 128 + 64 * half + lane_base;
-        const uint32_t vis[2] = {mt.seen[2 * half], mt.seen[2 * half + 1]};
-        const uint64_t* ks2 = reinterpret_cast<const uint64_t*>(mt.ks + 64 * half);
-        const uint64_t* vs2 = reinterpret_cast<const uint64_t*>(mt.vs + 64 * half);
-        // ---- the largest logit ----
-        float wm[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) wm[i] = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t sv[32];
-          tmem_ld32(tmem_s + 32 * c, sv);
+        const uint32_t tmem_s = tmem + (j & 1) * 128 + 64 * half + lane_base;
+        const uint32_t pst = sbase + Lay::kK + j % SK * kTileG + half * kHalfG + r_loc * 128;
+        const uint32_t plo = sbase + Lay::kPlo + half * kHalfG + r_loc * 128;
+        const uint32_t any = vis[0] | vis[1];
+        if (__any_sync(0xffffffffu, m == -INFINITY) && any) {
+          // the rows' first key (of this half): their reference, unless they have one
+          const int c = vis[0] ? __ffs(vis[0]) - 1 : 31 + __ffs(vis[1]);
+          uint32_t x;
+          asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(x) : "r"(tmem_s + c));
           tmem_wait_ld();
-          const bool all = vis[c] == 0xffffffffu;
-#pragma unroll
-          for (int q = 0; q < 16; ++q) {
-            const float2 w = unpair(mul2(pair(sv[2 * q], sv[2 * q + 1]), ks2[16 * c + q]));
-            wm[q & 3] = fmaxf(wm[q & 3], all || (vis[c] >> (2 * q) & 1u) ? w.x : -INFINITY);
-            wm[4 + (q & 3)] = fmaxf(wm[4 + (q & 3)], all || (vis[c] >> (2 * q + 1) & 1u) ? w.y : -INFINITY);
-          }
+          const float z = __uint_as_float(x) * a.scale_log2;
+          if (m == -INFINITY) m = fabsf(z) < 1e30f ? z : 0.f;
         }
-        const float zmax = rf * fmaxf(fmaxf(fmaxf(wm[0], wm[1]), fmaxf(wm[2], wm[3])),
-                                      fmaxf(fmaxf(wm[4], wm[5]), fmaxf(wm[6], wm[7])));
-        float alpha = 1.f;
-        bool look = false;  // whether P may leave its range: then the largest weight decides
-        if (zmax > m + 14.f) {  // also when the row has no reference yet
-          const float to = ceilf(zmax);
-          if (m == -INFINITY) {
-            lc = 1000.f;  // O is empty: the rule below picks the unit
-          } else {
-            l_run *= ex2f(m - to);
-            lc += to - m;  // O keeps its unit
-          }
-          m = to;
-        }
-        look = zmax > -INFINITY && (zmax - m + fmaxf(mt.emax[2 * half], mt.emax[2 * half + 1]) + lc > 14.f || lc > kMaxLc);
-        if (__any_sync(0xffffffffu, look)) {
-          float ymax = -INFINITY;  // the largest logit + exponent of its V scale
+        float tile_l = 0.f;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t sv[16];
-            tmem_ld16(tmem_s + 16 * c, sv);
+        for (int tries = 0; tries < 2; ++tries) {
+          const float neg_m = m == -INFINITY ? 0.f : -m;
+          const uint64_t neg2 = pair(neg_m, neg_m);
+          uint64_t ls[2] = {0ull, 0ull};
+          float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            uint32_t sv[32];
+            tmem_ld32(tmem_s + 32 * c, sv);
+            const uint32_t see = vis[c];
             tmem_wait_ld();
-            const uint32_t see = vis[c >> 1] >> (16 * (c & 1));
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int at = 64 * half + 16 * c + e;
-              const float y = fmaf(__uint_as_float(sv[e]) * mt.ks[at], rf, mt.ve[at]);
-              if (see >> e & 1u) ymax = fmaxf(ymax, y);
+            for (int q = 0; q < 4; ++q) {  // 8 keys: one 16-byte chunk of the row's P
+              float2 y[4];
+              uint32_t h[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int at = 8 * q + 2 * i;
+                float2 x = unpair(fma2(pair(__uint_as_float(sv[at]), __uint_as_float(sv[at + 1])), scale2, neg2));
+                if (see != 0xffffffffu) {
+                  if (!(see >> at & 1u)) x.x = -INFINITY;
+                  if (!(see >> (at + 1) & 1u)) x.y = -INFINITY;
+                }
+                top[i & 1] = fmaxf(fmaxf(x.x, x.y), top[i & 1]);
+                y[i] = make_float2(ex2f(x.x), ex2f(x.y));
+                h[i] = pack_bf16(y[i].x, y[i].y);
+                ls[i & 1] = add2(ls[i & 1], PRECISE ? pair(y[i].x, y[i].y) : pair(bf_lo(h[i]), bf_hi(h[i])));
+              }
+              const uint32_t off = (uint32_t)((4 * c + q) ^ (r_loc & 7)) << 4;
+              sts16(pst + off, h[0], h[1], h[2], h[3]);
+              if (PRECISE) {
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {  // what the parts before leave
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    y[i] = make_float2(y[i].x - bf_lo(h[i]), y[i].y - bf_hi(h[i]));
+                    h[i] = pack_bf16(y[i].x, y[i].y);
+                  }
+                  sts16(plo + part * kTileG + off, h[0], h[1], h[2], h[3]);
+                }
+              }
             }
           }
-          if (look && (ymax - m + lc > 14.f || lc > kMaxLc)) {
-            const float to = fmaxf(fminf(fminf(lc, m - ceilf(ymax) + 7.f), kMaxLc), -126.f);
-            alpha = ex2f(to - lc);
-            lc = to;
-          }
-          if (__any_sync(0xffffffffu, alpha != 1.f) && j > 0) {
+          const float2 l0 = unpair(ls[0]), l1 = unpair(ls[1]);
+          tile_l = (l0.x + l0.y) + (l1.x + l1.y);
+          const float up = fmaxf(top[0], top[1]);
+          if (!__any_sync(0xffffffffu, up > kRangeG) || tries) break;
+          // ---- some row's logits have left the range of its m: its sums move ----
+          const float alpha = up > kRangeG ? ex2f(-up) : 1.f;
+          if (up > kRangeG) m += up;
+          l_run *= alpha;
+          if (j > 0) {
             // the last tile's PV must have landed before O is rescaled
-            if (!warp_wait_g(&o_done[(j - 1) & 3], ((j - 1) >> 2) & 1)) {
-              failed = true;
-              break;
-            }
+            failed = !warp_wait_g(&o_done[(j - 1) & 3], ((j - 1) >> 2) & 1);
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < 8; ++c) {
@@ -445,104 +432,46 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
             tmem_wait_st();
           }
         }
-        // ---- P over this half of the consumed K tile ----
-        if (PRECISE && j > 0 && !warp_wait_g(&o_done[(j - 1) & 3], ((j - 1) >> 2) & 1)) {
-          failed = true;  // the low halves of the last tile are still being read
-          break;
-        }
-        const float neg_m = m == -INFINITY ? 0.f : -m;
-        const float unit_c = __int_as_float(((int)lc + 127) << 23);  // 2^lc
-        const uint64_t rf2 = pair(rf, rf), neg2 = pair(neg_m, neg_m), unit2 = pair(unit_c, unit_c);
-        const uint32_t pst = sbase + Lay::kStage + st * 2 * kTileG + half * kHalfG;
-        uint64_t ls[2] = {0ull, 0ull};
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t sv[32];
-          tmem_ld32(tmem_s + 32 * c, sv);
-          tmem_wait_ld();
-          const bool all = vis[c] == 0xffffffffu;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {  // 8 keys: one 16-byte chunk of the row's P
-            uint64_t pv[4];
-            uint32_t h[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int at = 4 * q + i;
-              const float2 x = unpair(fma2(mul2(pair(sv[2 * at], sv[2 * at + 1]), ks2[16 * c + at]), rf2, neg2));
-              float2 y = make_float2(ex2f(x.x), ex2f(x.y));
-              if (!all) {
-                y.x = vis[c] >> (2 * at) & 1u ? y.x : 0.f;
-                y.y = vis[c] >> (2 * at + 1) & 1u ? y.y : 0.f;
-              }
-              const uint64_t y2 = pair(y.x, y.y);
-              ls[i & 1] = add2(ls[i & 1], y2);
-              pv[i] = mul2(y2, mul2(vs2[16 * c + at], unit2));
-              const float2 f = unpair(pv[i]);
-              h[i] = pack_half2(f.x, f.y);
-            }
-            const uint32_t off = sw128_offset(r_loc, 4 * c + q);
-            sts16(pst + off, h[0], h[1], h[2], h[3]);
-            if (PRECISE) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float2 f = unpair(pv[i]), t = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-                h[i] = pack_half2(f.x - t.x, f.y - t.y);
-              }
-              sts16(sbase + Lay::kPlo + half * kHalfG + off, h[0], h[1], h[2], h[3]);
-            }
-          }
-        }
-        const float2 l0 = unpair(ls[0]), l1 = unpair(ls[1]);
-        l_run += (l0.x + l0.y) + (l1.x + l1.y);
+        if (failed) break;
+        l_run += tile_l;
         fence_proxy_async_smem();
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&s_free[st]);
-        mbar_arrive(&p_full[st]);
+        mbar_arrive(&s_free[j & 1]);
+        mbar_arrive(&p_full[j & 1]);
       }
     }
     // ---- the row's two key halves into one (m, l, o / l) in shared memory ----
     if (nt > 0 && !failed) failed = !warp_wait_g(&o_done[(nt - 1) & 3], ((nt - 1) >> 2) & 1);
     if (failed && lane == 0) report(a.status, kErrTimeout, kKernAttnQ8, blockIdx.x, 2, warp);
     tc_fence_after();
-    // every MMA is done (the barrier): the stages are free for the rows
-    float2* ml_s = reinterpret_cast<float2*>(smem + Lay::kMeta);  // [2][128]
-    float* o_s = reinterpret_cast<float*>(smem + Lay::kStage);
+    // every MMA is done (the barrier below): Q and the stages are free for the rows
+    float2* ml_s = reinterpret_cast<float2*>(smem + Lay::kMl);
+    float* o_s = reinterpret_cast<float*>(smem);  // [2][128][kORowG]
     ml_s[half * kQ8RowTile + r_loc] = make_float2(m, l_run);
     asm volatile("bar.sync 1, 256;" ::: "memory");
     const float2 other = ml_s[(half ^ 1) * kQ8RowTile + r_loc];
     const float M = fmaxf(m, other.x);
     const float mine = m == -INFINITY ? l_run : ex2f(m - M);  // an empty half: 0, or a NaN sum
     const float L = mine * l_run + (other.x == -INFINITY ? other.y : ex2f(other.x - M) * other.y);
-    // o's unit is 2^lc
-    const float f = (L == 0.f ? 0.f : mine / L) * __int_as_float((127 - (int)fmaxf(lc, -126.f)) << 23);
-    auto rows = [&](bool add) {
+    const float f = L == 0.f ? 0.f : mine / L;
+    if (active && nt > 0) {
+      float* dst = o_s + (half * kQ8RowTile + r_loc) * kORowG;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t ov[32];
         tmem_ld32(tmem_o + c * 32, ov);
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          float4* at = reinterpret_cast<float4*>(o_s + r_loc * kORowG + c * 32 + e);
-          float4 v = make_float4(__uint_as_float(ov[e]) * f, __uint_as_float(ov[e + 1]) * f,
-                                 __uint_as_float(ov[e + 2]) * f, __uint_as_float(ov[e + 3]) * f);
-          if (add) {
-            const float4 t = *at;
-            v.x += t.x, v.y += t.y, v.z += t.z, v.w += t.w;
-          }
-          *at = v;
-        }
+        for (int e = 0; e < 32; e += 4)
+          *reinterpret_cast<float4*>(dst + c * 32 + e) =
+              make_float4(__uint_as_float(ov[e]) * f, __uint_as_float(ov[e + 1]) * f, __uint_as_float(ov[e + 2]) * f,
+                          __uint_as_float(ov[e + 3]) * f);
       }
-    };
-    if (half == 1 && active && nt > 0) rows(false);
-    asm volatile("bar.sync 1, 256;" ::: "memory");
-    if (half == 0 && active) {
-      if (nt > 0) rows(true);
-      if (row_base + r_loc < a.R) __stcg(&a.pml[part * kQ8RowTile + r_loc], make_float2(M, L));
     }
+    if (half == 0 && row_base + r_loc < a.R) __stcg(&a.pml[part * kQ8RowTile + r_loc], make_float2(M, L));
   }
   tc_fence_before();
   __syncthreads();
@@ -551,11 +480,15 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
     tmem_dealloc(tmem, 512);
   }
   if (nt > 0) {
-    const float* o_s = reinterpret_cast<const float*>(smem + Lay::kStage);
+    const float* o_s = reinterpret_cast<const float*>(smem);
     const int n = min(kQ8RowTile, a.R - row_base) * (kDg / 4);
     float4* dst = reinterpret_cast<float4*>(a.po + part * kQ8RowTile * kDg);
-    for (int i = tid; i < n; i += kThreadsG)
-      __stcg(dst + i, *reinterpret_cast<const float4*>(o_s + i / (kDg / 4) * kORowG + i % (kDg / 4) * 4));
+    for (int i = tid; i < n; i += kThreadsG) {
+      const float* at = o_s + i / (kDg / 4) * kORowG + i % (kDg / 4) * 4;
+      const float4 x = *reinterpret_cast<const float4*>(at);
+      const float4 y = *reinterpret_cast<const float4*>(at + kQ8RowTile * kORowG);
+      __stcg(dst + i, make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w));
+    }
   }
 }
 
