@@ -1436,6 +1436,7 @@ sa_status sa_decode_attn_q8(const void* Q, const void* K8, const float* K_scale,
   a.out_f32 = out_dtype == SA_F32;
   a.n_split = p.n_split;
   a.chunk = p.chunk;
+  a.cluster = p.cluster;
   uint8_t* base = reinterpret_cast<uint8_t*>(ws);
   a.cnt = reinterpret_cast<uint32_t*>(base + kSmallCounterOffset);
   a.po = reinterpret_cast<float*>(base + SA_WS_HEADER_BYTES);

@@ -9,7 +9,7 @@
 // halves of O in TMEM), so what is left is latency: a slice of an index is a
 // handful of tiles.
 //
-//   * Warps 9-12 (producers) load the codes of a tile straight into registers
+//   * Warps 9-16 (producers) load the codes of a tile straight into registers
 //     (16 bytes a lane, the next K and V pieces in flight while the last ones
 //     are stored) and write scale * code as bf16: exact for the powers of two
 //     an append writes (4 significant bits), so S and PV see the cache's own
@@ -24,9 +24,10 @@
 //   * bf16 outputs: weights are rounded to bf16, 8 bits, and l is the sum of
 //     the rounded ones, so that they add up to one.  fp32 outputs: three bf16
 //     parts (24 bits), for whose shared memory K has one stage instead of two.
-//   * Each row leaves its slice's (m, l, o / l) in the workspace, and a second
-//     kernel merges them.  It is launched with programmatic dependence and
-//     reads one row per warp, so the merge uses the whole GPU and no counters.
+//   * The key slices of 128 rows are a cluster of up to 8 CTAs: each leaves its
+//     rows' (m, l, o / l) in its shared memory and merges 128 / 8 rows of all
+//     of them.  More slices than that (few rows over a long context) go
+//     through the workspace and a second kernel, one row per warp.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -43,11 +44,11 @@ using namespace wm;
 
 constexpr int kDg = 128;
 constexpr int kKeysG = 128;     // keys of a tile
-constexpr int kSoftWarps = 8, kMmaWarp = 8, kProdWarp = 9, kProdWarps = 4;
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kProdWarp = 9, kProdWarps = 8;
 constexpr int kThreadsG = 32 * (kProdWarp + kProdWarps);
 constexpr int kPer = 128 * 8 / (32 * kProdWarps);  // 16-byte pieces of a K (or V) tile a producer holds
 constexpr int kRowStep = 128 / kPer;
-static_assert(32 * kProdWarps == kKeysG, "one producer thread per key's token and scales");
+static_assert(32 * kProdWarps >= kKeysG, "one producer thread per key's token and scales");
 constexpr int kHalfG = 16384;   // 128 rows x 128 bytes
 constexpr int kTileG = 2 * kHalfG;
 constexpr float kRangeG = 30.f;  // log2 units a logit may pass its row's m by
@@ -55,18 +56,18 @@ constexpr int kORowG = kDg + 4;  // floats of an output row in shared memory
 
 template <bool PRECISE>
 struct SmemG {
-  static constexpr int kStagesK = PRECISE ? 1 : 2, kStagesV = 2;
+  static constexpr int kStagesK = PRECISE ? 1 : 3, kStagesV = 2;
   static constexpr int kParts = PRECISE ? 3 : 1;         // of P: the first over the K tile
   static constexpr int kK = kTileG;                      // after Q
   static constexpr int kV = kK + kStagesK * kTileG;
   static constexpr int kPlo = kV + kStagesV * kTileG;
   static constexpr int kTok = kPlo + (kParts - 1) * kTileG;  // [2][128]: tokens of a tile's keys, -1 for none
   static constexpr int kScale = kTok + 2 * kKeysG * 4;       // [2][128]: their (K, V) scales
-  static constexpr int kSeen = kScale + 2 * kKeysG * 8;      // [2][4]: bit c of word w: key 32w + c is a token
-  static constexpr int kMl = kSeen + 2 * 4 * 4;              // [2][128]: (m, l) of the rows' key halves
-  // k_full[2] v_full[2] k_empty[2] v_empty[2] s_full[2] s_free[2] p_full[2] o_done[4] q_full
-  static constexpr int kBar = kMl + 2 * kQ8RowTile * 8;
-  static constexpr int kSlot = kBar + 8 * 19;
+  static constexpr int kSeen = kScale + 2 * kKeysG * 8;      // [4 tiles][4]: bit c of word w: key 32w + c is a token
+  static constexpr int kMl = kSeen + 4 * 4 * 4;              // [3][128]: (m, l) of the rows' key halves, and of the rows
+  // k_full[3] k_empty[3] v_full[2] v_empty[2] s_full[2] s_free[2] p_full[2] o_done[4] q_full
+  static constexpr int kBar = kMl + 3 * kQ8RowTile * 8;
+  static constexpr int kSlot = kBar + 8 * 21;
   static constexpr size_t kBytes = 1024 + kSlot + 16;
   static_assert(kBytes <= 232448, "shared memory budget");
   static_assert(2 * kQ8RowTile * kORowG * 4 <= kTok, "the output rows fit over Q and the stages");
@@ -105,6 +106,15 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uin
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d));
 }
 
+// Waits for the TMEM loads so far; the values of v are used only behind it.
+__device__ __forceinline__ void tmem_wait(uint32_t (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+               :
+               : "memory");
+}
+
 __device__ __forceinline__ bool warp_wait_g(uint64_t* bar, uint32_t parity) {
   bool ok = true;
   if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, kWaitLimitNs);
@@ -133,6 +143,37 @@ __device__ __forceinline__ void store_codes(uint32_t tile, int r, int c, const u
   sts16(base + sw128_offset(r, (c & 3) * 2 + 1), b[4], b[5], b[6], b[7]);
 }
 
+// dims 4 * lane .. of a query row's output
+__device__ __forceinline__ void store_row(const Q8AttnArgs& a, int b, int g, int row, int lane, const float4& v) {
+  const int64_t off = (((int64_t)(row / a.G) * a.B + b) * a.Hq + g * a.G + row % a.G) * kDg + 4 * lane;
+  if (a.out_f32)
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.O) + off) = v;
+  else
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.O) + off) =
+        make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+}
+
+// shared memory of the cluster's CTA `rank`, at this CTA's address
+__device__ __forceinline__ float4 ld_peer4(uint32_t addr, int rank) {
+  uint32_t at;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at));
+  return v;
+}
+__device__ __forceinline__ float2 ld_peer2(uint32_t addr, int rank) {
+  uint32_t at;
+  float2 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 template <bool PRECISE>
 __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8AttnArgs a, const int row_tiles) {
   using Lay = SmemG<PRECISE>;
@@ -142,9 +183,9 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
   const uint32_t sbase = smem_u32(smem);
   uint32_t* seen_s = reinterpret_cast<uint32_t*>(smem + Lay::kSeen);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + Lay::kBar);
-  uint64_t* v_full = k_full + 2;
-  uint64_t* k_empty = v_full + 2;
-  uint64_t* v_empty = k_empty + 2;
+  uint64_t* k_empty = k_full + 3;
+  uint64_t* v_full = k_empty + 3;
+  uint64_t* v_empty = v_full + 2;
   uint64_t* s_full = v_empty + 2;
   uint64_t* s_free = s_full + 2;
   uint64_t* p_full = s_free + 2;
@@ -163,10 +204,12 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
   if (warp == kMmaWarp) {
     tmem_alloc(slot, 512);
     if (lane == 0) {
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 3; ++i) {
         mbar_init(&k_full[i], kProdWarps);
-        mbar_init(&v_full[i], kProdWarps);
         mbar_init(&k_empty[i], 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&v_full[i], kProdWarps);
         mbar_init(&v_empty[i], 1);
         mbar_init(&s_full[i], 1);
         mbar_init(&s_free[i], kSoftWarps);
@@ -183,10 +226,12 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
   const int n_keys = !s.ok ? 0 : a.idx ? a.k : s.len;  // entries, or tokens
   const int e_beg = (int)min((int64_t)n_keys, (int64_t)slice * a.chunk), e_end = min(n_keys, e_beg + a.chunk);
   const int nt = (e_end - e_beg + kKeysG - 1) / kKeysG;
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *slot;
+  // every role meets here once its first loads are on their way: barriers and TMEM are ready
+  auto ready = [] {
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  };
 
   if (warp >= kProdWarp) {
     // =============== producers ===============
@@ -198,7 +243,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
     // this thread's key of tile j: its token as listed (it loads the key's scales too)
     auto token = [&](int j) -> int {
       const int e = e_beg + j * kKeysG + pt;
-      if (e >= e_end) return -1;
+      if (pt >= kKeysG || e >= e_end) return -1;
       return a.idx ? __ldcg(&a.idx[(int64_t)b * a.k + e]) : e;
     };
     auto sync = [] { asm volatile("bar.sync 2, %0;" ::"n"(32 * kProdWarps) : "memory"); };
@@ -221,11 +266,12 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
       }
     };
     int tm = token(0), tm_next = token(1);
-    tok_s[pt] = tm < s.len ? tm : -1;
+    if (pt < kKeysG) tok_s[pt] = tm < s.len ? tm : -1;
     sync();
     fetch(a.K, 0, kv);
     scales(tm);
     fetch(a.V, 0, vv);
+    ready();
     bool dead = false;
     for (int j = 0; j < nt; ++j) {
       const int sk = j % SK, sv = j % SV;
@@ -234,17 +280,15 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
           report(a.status, kErrDevice, kKernAttnQ8, (int64_t)b * a.k + e_beg + j * kKeysG + pt, tm, s.len);
         tm = -1;
       }
-      scale_s[(j & 1) * kKeysG + pt] = make_float2(ks, vs);
+      if (pt < kKeysG) scale_s[(j & 1) * kKeysG + pt] = make_float2(ks, vs);
       const uint32_t seen = __ballot_sync(0xffffffffu, tm >= 0);
-      if (!dead && ((j >= SK && !warp_wait_g(&k_empty[sk], (j / SK - 1) & 1)) ||
-                    (j >= SV && !warp_wait_g(&v_empty[sv], (j / SV - 1) & 1)))) {
+      if (!dead && j >= SK && !warp_wait_g(&k_empty[sk], (j / SK - 1) & 1)) {
         if (lane == 0) report(a.status, kErrTimeout, kKernAttnQ8, blockIdx.x, 0, j);
         dead = true;  // only meets the other producers from here on
       }
-      if (lane == 0 && !dead) seen_s[(j & 1) * 4 + (pt >> 5)] = seen;
+      if (pt < kKeysG && lane == 0 && !dead) seen_s[(j & 3) * 4 + (pt >> 5)] = seen;
       tm = tm_next;
-      const int t = tm < s.len ? tm : -1;
-      tok_s[((j + 1) & 1) * kKeysG + pt] = t;
+      if (pt < kKeysG) tok_s[((j + 1) & 1) * kKeysG + pt] = tm < s.len ? tm : -1;
       sync();
       if (dead) continue;
       const float2* sc = scale_s + (j & 1) * kKeysG + pr;
@@ -257,6 +301,11 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
       fetch(a.K, j + 1, kv);
       scales(tm);
       tm_next = token(j + 2);
+      if (j >= SV && !warp_wait_g(&v_empty[sv], (j / SV - 1) & 1)) {
+        if (lane == 0) report(a.status, kErrTimeout, kKernAttnQ8, blockIdx.x, 3, j);
+        dead = true;
+        continue;
+      }
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
         store_codes(sbase + Lay::kV + sv * kTileG, pr + kRowStep * i, pc, vv[i], sc[kRowStep * i].y);
@@ -267,6 +316,8 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
     }
   } else if (warp == kMmaWarp) {
     // =============== MMA issuer ===============
+    ready();
+    const uint32_t tmem = *slot;
     if (lane == 0 && nt > 0) {
       constexpr uint32_t idesc_qk = umma_idesc_bf16(128, 128, false, false);
       constexpr uint32_t idesc_pv = umma_idesc_bf16(128, 128, false, true);
@@ -316,7 +367,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
     }
   } else {
     // =============== queries, then softmax ===============
-    if (nt > 0) {
+    {
       const int r = tid >> 1, qh = tid & 1;  // half a query row: dims 64 qh ..
       const int row = row_base + r;
       uint4 qv[8];
@@ -327,6 +378,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
 #pragma unroll
         for (int i = 0; i < 8; ++i) qv[i] = __ldcg(reinterpret_cast<const uint4*>(a.Q + off) + i);
       }
+      ready();
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         sts16(sbase + qh * kHalfG + sw128_offset(r, i), qv[i].x, qv[i].y, qv[i].z, qv[i].w);
@@ -334,6 +386,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
     }
+    const uint32_t tmem = *slot;
     const int half = warp >> 2;
     const int r_loc = (warp & 3) * 32 + lane;
     const bool active = row_base + (warp & 3) * 32 < a.R;
@@ -348,7 +401,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
         break;
       }
       tc_fence_after();
-      const uint32_t* vis = seen_s + (j & 1) * 4 + 2 * half;
+      const uint32_t* vis = seen_s + (j & 3) * 4 + 2 * half;
       if (active) {
         const uint32_t tmem_s = tmem + (j & 1) * 128 + 64 * half + lane_base;
         const uint32_t pst = sbase + Lay::kK + j % SK * kTileG + half * kHalfG + r_loc * 128;
@@ -370,21 +423,17 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
           const uint64_t neg2 = pair(neg_m, neg_m);
           uint64_t ls[2] = {0ull, 0ull};
           float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
-            uint32_t sv[32];
-            tmem_ld32(tmem_s + 32 * c, sv);
-            const uint32_t see = vis[c];
-            tmem_wait_ld();
+          auto weights = [&](const uint32_t (&sv)[16], int c) {  // of keys 16c .. of this half
+            const uint32_t see = vis[c >> 1] >> (16 * (c & 1)) & 0xffffu;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {  // 8 keys: one 16-byte chunk of the row's P
+            for (int q = 0; q < 2; ++q) {  // 8 keys: one 16-byte chunk of the row's P
               float2 y[4];
               uint32_t h[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int at = 8 * q + 2 * i;
                 float2 x = unpair(fma2(pair(__uint_as_float(sv[at]), __uint_as_float(sv[at + 1])), scale2, neg2));
-                if (see != 0xffffffffu) {
+                if (see != 0xffffu) {
                   if (!(see >> at & 1u)) x.x = -INFINITY;
                   if (!(see >> (at + 1) & 1u)) x.y = -INFINITY;
                 }
@@ -393,7 +442,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
                 h[i] = pack_bf16(y[i].x, y[i].y);
                 ls[i & 1] = add2(ls[i & 1], PRECISE ? pair(y[i].x, y[i].y) : pair(bf_lo(h[i]), bf_hi(h[i])));
               }
-              const uint32_t off = (uint32_t)((4 * c + q) ^ (r_loc & 7)) << 4;
+              const uint32_t off = (uint32_t)((2 * c + q) ^ (r_loc & 7)) << 4;
               sts16(pst + off, h[0], h[1], h[2], h[3]);
               if (PRECISE) {
 #pragma unroll
@@ -407,7 +456,21 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
                 }
               }
             }
-          }
+          };
+          // a load of TMEM takes about as long as 16 keys' weights: one ahead
+          uint32_t sa[16], sb[16];
+          tmem_ld16(tmem_s, sa);
+          tmem_wait(sa);
+          tmem_ld16(tmem_s + 16, sb);
+          weights(sa, 0);
+          tmem_wait(sb);
+          tmem_ld16(tmem_s + 32, sa);
+          weights(sb, 1);
+          tmem_wait(sa);
+          tmem_ld16(tmem_s + 48, sb);
+          weights(sa, 2);
+          tmem_wait(sb);
+          weights(sb, 3);
           const float2 l0 = unpair(ls[0]), l1 = unpair(ls[1]);
           tile_l = (l0.x + l0.y) + (l1.x + l1.y);
           const float up = fmaxf(top[0], top[1]);
@@ -460,30 +523,72 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
     if (active && nt > 0) {
       float* dst = o_s + (half * kQ8RowTile + r_loc) * kORowG;
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        uint32_t ov[32];
-        tmem_ld32(tmem_o + c * 32, ov);
-        tmem_wait_ld();
+      for (int c = 0; c < kDg; c += 32) {
+        uint32_t oa[16], ob[16];
+        tmem_ld16(tmem_o + c, oa);
+        tmem_ld16(tmem_o + c + 16, ob);
+        tmem_wait(oa);
+        tmem_wait(ob);
 #pragma unroll
-        for (int e = 0; e < 32; e += 4)
-          *reinterpret_cast<float4*>(dst + c * 32 + e) =
-              make_float4(__uint_as_float(ov[e]) * f, __uint_as_float(ov[e + 1]) * f, __uint_as_float(ov[e + 2]) * f,
-                          __uint_as_float(ov[e + 3]) * f);
+        for (int e = 0; e < 16; e += 4) {
+          *reinterpret_cast<float4*>(dst + c + e) =
+              make_float4(__uint_as_float(oa[e]) * f, __uint_as_float(oa[e + 1]) * f, __uint_as_float(oa[e + 2]) * f,
+                          __uint_as_float(oa[e + 3]) * f);
+          *reinterpret_cast<float4*>(dst + c + 16 + e) =
+              make_float4(__uint_as_float(ob[e]) * f, __uint_as_float(ob[e + 1]) * f, __uint_as_float(ob[e + 2]) * f,
+                          __uint_as_float(ob[e + 3]) * f);
+        }
       }
     }
-    if (half == 0 && row_base + r_loc < a.R) __stcg(&a.pml[part * kQ8RowTile + r_loc], make_float2(M, L));
+    if (half == 0) ml_s[2 * kQ8RowTile + r_loc] = make_float2(M, L);
   }
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(*slot, 512);
   }
+  const int rows = min(kQ8RowTile, a.R - row_base);
+  if (a.cluster) {
+    // ---- the slices' rows: this CTA merges every a.cluster-th part of them ----
+    if (a.cluster > 1) cluster_sync();  // every slice's rows are in its shared memory
+    const int n = a.cluster, per = kQ8RowTile / n;
+    const uint32_t ml_at = smem_u32(smem + Lay::kMl) + 2 * kQ8RowTile * 8;
+    for (int r = slice * per + warp; r < min(rows, (slice + 1) * per); r += kThreadsG / 32) {
+      float mm[8], w[8], M = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        mm[i] = -INFINITY, w[i] = 0.f;
+        if (i < n) {
+          const float2 ml = ld_peer2(ml_at + r * 8, i);
+          mm[i] = ml.x, w[i] = ml.y;
+          M = fmaxf(M, ml.x);
+        }
+      }
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        w[i] *= mm[i] == -INFINITY ? 0.f : ex2f(mm[i] - M);
+        L += w[i];
+        if (i < n && w[i] != 0.f) {  // else that slice has no row there
+          const uint32_t at = sbase + (r * kORowG + 4 * lane) * 4;
+          const float4 x = ld_peer4(at, i), y = ld_peer4(at + kQ8RowTile * kORowG * 4, i);
+          acc.x += w[i] * (x.x + y.x), acc.y += w[i] * (x.y + y.y);
+          acc.z += w[i] * (x.z + y.z), acc.w += w[i] * (x.w + y.w);
+        }
+      }
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      store_row(a, b, g, row_base + r, lane, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+    }
+    if (a.cluster > 1) cluster_sync();  // no CTA leaves while its rows are read
+    return;
+  }
+  const float2* ml_s = reinterpret_cast<const float2*>(smem + Lay::kMl) + 2 * kQ8RowTile;
+  if (tid < rows) __stcg(&a.pml[part * kQ8RowTile + tid], ml_s[tid]);
   if (nt > 0) {
     const float* o_s = reinterpret_cast<const float*>(smem);
-    const int n = min(kQ8RowTile, a.R - row_base) * (kDg / 4);
     float4* dst = reinterpret_cast<float4*>(a.po + part * kQ8RowTile * kDg);
-    for (int i = tid; i < n; i += kThreadsG) {
+    for (int i = tid; i < rows * (kDg / 4); i += kThreadsG) {
       const float* at = o_s + i / (kDg / 4) * kORowG + i % (kDg / 4) * 4;
       const float4 x = *reinterpret_cast<const float4*>(at);
       const float4 y = *reinterpret_cast<const float4*>(at + kQ8RowTile * kORowG);
@@ -526,52 +631,54 @@ __global__ void __launch_bounds__(256) attn_q8_merge_kernel(const Q8AttnArgs a, 
     }
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
-  const int64_t off = (((int64_t)(row / a.G) * a.B + b) * a.Hq + g * a.G + row % a.G) * kDg + 4 * lane;
-  if (a.out_f32)
-    *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.O) + off) =
-        make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-  else
-    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.O) + off) =
-        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-}
-
-template <typename... Exp, typename... Act>
-cudaError_t launch_pdl(void (*kern)(Exp...), unsigned grid, unsigned threads, size_t smem, cudaStream_t stream,
-                       Act... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1] = {pdl_attribute()};
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  store_row(a, b, g, row, lane, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
 }
 
 }  // namespace
 
-// One CTA per SM and one wave, at most the 128-key tiles there are.
+// One CTA per SM and one wave, at most the 128-key tiles there are.  A cluster
+// of 1, 2, 4 or 8 slices merges in shared memory; more slices only where the
+// cluster's would be longer than four tiles.
 void plan_attn_q8_group(Q8AttnPlan& p, int64_t n, int sms) {
   const int64_t tiles = n > 0 ? (n + kKeysG - 1) / kKeysG : 1;
   int64_t split = sms / p.units > 1 ? sms / p.units : 1;
   if (split > tiles) split = tiles;
+  p.cluster = 0;
+  if (split <= 8 || tiles <= 8 * 4) {
+    p.cluster = split >= 8 ? 8 : split >= 4 ? 4 : split >= 2 ? 2 : 1;
+    split = p.cluster;
+  }
   p.chunk = (int)((tiles + split - 1) / split) * kKeysG;
-  p.n_split = (int)((tiles * kKeysG + p.chunk - 1) / p.chunk);
-  p.parts = p.n_split;
+  p.n_split = p.cluster ? p.cluster : (int)((tiles * kKeysG + p.chunk - 1) / p.chunk);
+  p.parts = p.cluster ? 0 : p.n_split;
   p.rows = kQ8RowTile;
 }
 
 cudaError_t launch_attn_q8_group(const Q8AttnArgs& a, const Q8AttnPlan& p, cudaStream_t stream) {
   auto kern = a.out_f32 ? attn_q8_group_kernel<true> : attn_q8_group_kernel<false>;
-  const size_t smem = a.out_f32 ? SmemG<true>::kBytes : SmemG<false>::kBytes;
-  cudaError_t e = ensure_smem(kern, smem);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.units * p.n_split));
+  cfg.blockDim = dim3(kThreadsG);
+  cfg.dynamicSmemBytes = a.out_f32 ? SmemG<true>::kBytes : SmemG<false>::kBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2] = {pdl_attribute()};
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.cluster ? p.cluster : 1;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaError_t e = ensure_smem(kern, cfg.dynamicSmemBytes);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(kern, (unsigned)(p.units * p.n_split), kThreadsG, smem, stream, a, p.row_tiles);
-  if (e != cudaSuccess) return e;
+  e = cudaLaunchKernelEx(&cfg, kern, a, p.row_tiles);
+  if (e != cudaSuccess || p.cluster) return e != cudaSuccess ? e : cudaGetLastError();
   const int n_rows = a.B * a.Hkv * a.R;
-  return launch_pdl(attn_q8_merge_kernel, (unsigned)((n_rows + 7) / 8), 256, 0, stream, a, p.row_tiles, n_rows);
+  cfg.gridDim = dim3((unsigned)((n_rows + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, attn_q8_merge_kernel, a, p.row_tiles, n_rows);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace sa

@@ -148,6 +148,7 @@ struct Q8AttnArgs {
   void* O;
   int out_f32;
   int n_split, chunk;  // key slices of chunk keys (of the index entries, or of the tokens)
+  int cluster;         // attn_q8_group.cu: slices that merge as a cluster (0: through the workspace)
   // n_split > 1: counters per (b, g, row tile), zero between launches, and
   // the slices' partials [unit][n_split][rows][128], (m, l) [unit][n_split][rows]
   uint32_t* cnt;
@@ -157,7 +158,7 @@ struct Q8AttnArgs {
 };
 struct Q8AttnPlan {
   bool group;  // attn_q8_group.cu
-  int row_tiles, units, n_split, chunk;
+  int row_tiles, units, n_split, chunk, cluster;
   int parts, rows;  // partial results of a unit, and the query rows of each (padded)
 };
 Q8AttnPlan plan_attn_q8(int R, int B, int Hkv, int64_t n_tokens, int S_max, int k, int sms, int max_counters);
