@@ -5,9 +5,8 @@
 // What bounds it: with R rows a (token, KV head) costs 256 + 8/64 bytes and
 // 512 R flops.  From about 16 rows the warp-level MMAs of attn_q8.cu, whose
 // warps each convert all codes they multiply, are issue-bound; here each code
-// is converted once per 128 rows and the products run on tcgen05 (S and both
-// halves of O in TMEM), so what is left is latency: a slice of an index is a
-// handful of tiles.
+// is converted once per 128 rows and the products run on tcgen05 (S and O in
+// TMEM), so what is left is latency: a slice of an index is a handful of tiles.
 //
 //   * Warps 9-16 (producers) load the codes of a tile straight into registers
 //     (16 bytes a lane, the next K and V pieces in flight while the last ones
@@ -15,12 +14,13 @@
 //     an append writes (4 significant bits), so S and PV see the cache's own
 //     values and the softmax no scales.  K as [keys, d] K-major, V the same
 //     rows read MN-major, 128-byte swizzled.
-//   * Warp 8 issues S = Q K^T and, per key half h, O_h += P_h V_h.
+//   * Warp 8 issues S = Q K^T and O += P V.
 //   * Warps 0-7: softmax, one query row per thread and key half, P written
 //     over the consumed K tile.  One pass: weights are 2^(z - m) with m the
 //     row's first logit until one passes it by 30 (fp32 and bf16 have the
 //     exponents for that); only then the row's sums move to a new m and the
-//     tile's weights are made again.
+//     tile's weights are made again.  Both halves of a row keep one m: its two
+//     warps meet once a tile to agree on that.
 //   * bf16 outputs: weights are rounded to bf16, 8 bits, and l is the sum of
 //     the rounded ones, so that they add up to one.  fp32 outputs: three bf16
 //     parts (24 bits), for whose shared memory K has one stage instead of two.
@@ -64,13 +64,14 @@ struct SmemG {
   static constexpr int kTok = kPlo + (kParts - 1) * kTileG;  // [2][128]: tokens of a tile's keys, -1 for none
   static constexpr int kScale = kTok + 2 * kKeysG * 4;       // [2][128]: their (K, V) scales
   static constexpr int kSeen = kScale + 2 * kKeysG * 8;      // [4 tiles][4]: bit c of word w: key 32w + c is a token
-  static constexpr int kMl = kSeen + 4 * 4 * 4;              // [3][128]: (m, l) of the rows' key halves, and of the rows
+  static constexpr int kMove = kSeen + 4 * 4 * 4;            // [2 tiles][8 warps]: a row of the warp leaves its range
+  static constexpr int kMl = kMove + 2 * 8 * 4;              // [2][128] floats of the rows' halves, [128] (m, l)
   // k_full[3] k_empty[3] v_full[2] v_empty[2] s_full[2] s_free[2] p_full[2] o_done[4] q_full
-  static constexpr int kBar = kMl + 3 * kQ8RowTile * 8;
+  static constexpr int kBar = kMl + 2 * kQ8RowTile * 8;
   static constexpr int kSlot = kBar + 8 * 21;
   static constexpr size_t kBytes = 1024 + kSlot + 16;
   static_assert(kBytes <= 232448, "shared memory budget");
-  static_assert(2 * kQ8RowTile * kORowG * 4 <= kTok, "the output rows fit over Q and the stages");
+  static_assert(kQ8RowTile * kORowG * 4 <= kTok, "the output rows fit over Q and the stages");
 };
 
 // two floats at once
@@ -160,14 +161,15 @@ __device__ __forceinline__ float4 ld_peer4(uint32_t addr, int rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(at));
+               : "r"(at)
+               : "memory");
   return v;
 }
 __device__ __forceinline__ float2 ld_peer2(uint32_t addr, int rank) {
   uint32_t at;
   float2 v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at));
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
   return v;
 }
 __device__ __forceinline__ void cluster_sync() {
@@ -241,10 +243,13 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
     int* tok_s = reinterpret_cast<int*>(smem + Lay::kTok);
     float2* scale_s = reinterpret_cast<float2*>(smem + Lay::kScale);
     // this thread's key of tile j: its token as listed (it loads the key's scales too)
+    // (an index's entries need nothing of the sequence: their loads do not wait for it)
+    const int64_t first = (int64_t)slice * a.chunk + pt;
+    const int64_t end = pt < kKeysG ? min((int64_t)(a.idx ? a.k : s.len), (int64_t)(slice + 1) * a.chunk) : 0;
     auto token = [&](int j) -> int {
-      const int e = e_beg + j * kKeysG + pt;
-      if (pt >= kKeysG || e >= e_end) return -1;
-      return a.idx ? __ldcg(&a.idx[(int64_t)b * a.k + e]) : e;
+      const int64_t e = first + j * kKeysG;
+      if (e >= end) return -1;
+      return a.idx ? __ldcg(&a.idx[(int64_t)b * a.k + e]) : (int)e;
     };
     auto sync = [] { asm volatile("bar.sync 2, %0;" ::"n"(32 * kProdWarps) : "memory"); };
     auto fetch = [&](const uint8_t* codes, int j, uint4 (&v)[kPer]) {
@@ -335,10 +340,10 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
             const uint64_t vd = umma_desc_sw128(vst + h * 8192 + kk * 2048, kHalfG, 1024);
 #pragma unroll
             for (int q = 0; q < Lay::kParts; ++q)
-              umma_bf16(tmem + 256 + 128 * h,
+              umma_bf16(tmem + 256,
                         umma_desc_sw128((q == 0 ? pst : sbase + Lay::kPlo + (q - 1) * kTileG) + h * kHalfG + kk * 32, 16,
                                         1024),
-                        vd, idesc_pv, (i | kk | q) != 0);
+                        vd, idesc_pv, (i | h | kk | q) != 0);
           }
         umma_commit(&k_empty[i % SK]);
         umma_commit(&v_empty[i % SV]);
@@ -391,28 +396,33 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
     const int r_loc = (warp & 3) * 32 + lane;
     const bool active = row_base + (warp & 3) * 32 < a.R;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tmem_o = tmem + 256 + 128 * half + lane_base;
+    const uint32_t tmem_o = tmem + 256 + 64 * half + lane_base;  // this thread's columns of O
+    volatile float* up_s = reinterpret_cast<volatile float*>(smem + Lay::kMl) + r_loc;  // [2][128], by half
+    volatile uint32_t* move_s = reinterpret_cast<volatile uint32_t*>(smem + Lay::kMove);  // [2 tiles][8 warps]
+    auto meet = [&] { asm volatile("bar.sync %0, 64;" ::"r"(3 + (warp & 3)) : "memory"); };  // the rows' two warps
     const uint64_t scale2 = pair(a.scale_log2, a.scale_log2);
     float m = -INFINITY, l_run = 0.f;
+    // a wait that gave up: the warp goes on without waiting (on garbage, which
+    // the status tells), so that no other warp waits for it at a barrier
     bool failed = false;
     for (int j = 0; j < nt; ++j) {
-      if (!warp_wait_g(&s_full[j & 1], (j >> 1) & 1) || !warp_wait_g(&k_full[j % SK], (j / SK) & 1)) {
-        failed = true;
-        break;
-      }
+      if (!failed) failed = !warp_wait_g(&s_full[j & 1], (j >> 1) & 1) || !warp_wait_g(&k_full[j % SK], (j / SK) & 1);
       tc_fence_after();
-      const uint32_t* vis = seen_s + (j & 3) * 4 + 2 * half;
+      const uint32_t* seen = seen_s + (j & 3) * 4;
+      const uint32_t* vis = seen + 2 * half;
       if (active) {
         const uint32_t tmem_s = tmem + (j & 1) * 128 + 64 * half + lane_base;
         const uint32_t pst = sbase + Lay::kK + j % SK * kTileG + half * kHalfG + r_loc * 128;
         const uint32_t plo = sbase + Lay::kPlo + half * kHalfG + r_loc * 128;
-        const uint32_t any = vis[0] | vis[1];
-        if (__any_sync(0xffffffffu, m == -INFINITY) && any) {
-          // the rows' first key (of this half): their reference, unless they have one
-          const int c = vis[0] ? __ffs(vis[0]) - 1 : 31 + __ffs(vis[1]);
+        if (__any_sync(0xffffffffu, m == -INFINITY) && (seen[0] | seen[1] | seen[2] | seen[3])) {
+          // the rows' first key: their reference
+          int c = 0;
+          while (seen[c] == 0u) ++c;
           uint32_t x;
-          asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(x) : "r"(tmem_s + c));
-          tmem_wait_ld();
+          asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];"
+                       : "=r"(x)
+                       : "r"(tmem_s - 64 * half + 32 * c + __ffs(seen[c]) - 1));
+          asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(x) : : "memory");
           const float z = __uint_as_float(x) * a.scale_log2;
           if (m == -INFINITY) m = fabsf(z) < 1e30f ? z : 0.f;
         }
@@ -473,29 +483,35 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
           weights(sb, 3);
           const float2 l0 = unpair(ls[0]), l1 = unpair(ls[1]);
           tile_l = (l0.x + l0.y) + (l1.x + l1.y);
-          const float up = fmaxf(top[0], top[1]);
-          if (!__any_sync(0xffffffffu, up > kRangeG) || tries) break;
+          if (tries) break;
+          const float mine = fmaxf(top[0], top[1]);
+          const bool move = __any_sync(0xffffffffu, mine > kRangeG);
+          if (lane == 0) move_s[(j & 1) * 8 + warp] = move;
+          meet();
+          if (!move && !move_s[(j & 1) * 8 + (warp ^ 4)]) break;
           // ---- some row's logits have left the range of its m: its sums move ----
+          up_s[half * kQ8RowTile] = mine;
+          meet();
+          const float up = fmaxf(mine, up_s[(half ^ 1) * kQ8RowTile]);
           const float alpha = up > kRangeG ? ex2f(-up) : 1.f;
           if (up > kRangeG) m += up;
           l_run *= alpha;
           if (j > 0) {
             // the last tile's PV must have landed before O is rescaled
-            failed = !warp_wait_g(&o_done[(j - 1) & 3], ((j - 1) >> 2) & 1);
+            if (!failed) failed = !warp_wait_g(&o_done[(j - 1) & 3], ((j - 1) >> 2) & 1);
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
+            for (int c = 0; c < 64; c += 16) {
               uint32_t ov[16];
-              tmem_ld16(tmem_o + c * 16, ov);
-              tmem_wait_ld();
+              tmem_ld16(tmem_o + c, ov);
+              tmem_wait(ov);
 #pragma unroll
               for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-              tmem_st16(tmem_o + c * 16, ov);
+              tmem_st16(tmem_o + c, ov);
             }
             tmem_wait_st();
           }
         }
-        if (failed) break;
         l_run += tile_l;
         fence_proxy_async_smem();
       }
@@ -506,24 +522,20 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
         mbar_arrive(&p_full[j & 1]);
       }
     }
-    // ---- the row's two key halves into one (m, l, o / l) in shared memory ----
+    // ---- the row's (m, l, o / l) into shared memory ----
     if (nt > 0 && !failed) failed = !warp_wait_g(&o_done[(nt - 1) & 3], ((nt - 1) >> 2) & 1);
     if (failed && lane == 0) report(a.status, kErrTimeout, kKernAttnQ8, blockIdx.x, 2, warp);
     tc_fence_after();
     // every MMA is done (the barrier below): Q and the stages are free for the rows
-    float2* ml_s = reinterpret_cast<float2*>(smem + Lay::kMl);
-    float* o_s = reinterpret_cast<float*>(smem);  // [2][128][kORowG]
-    ml_s[half * kQ8RowTile + r_loc] = make_float2(m, l_run);
+    float* l_s = reinterpret_cast<float*>(smem + Lay::kMl) + r_loc;
+    l_s[half * kQ8RowTile] = l_run;
     asm volatile("bar.sync 1, 256;" ::: "memory");
-    const float2 other = ml_s[(half ^ 1) * kQ8RowTile + r_loc];
-    const float M = fmaxf(m, other.x);
-    const float mine = m == -INFINITY ? l_run : ex2f(m - M);  // an empty half: 0, or a NaN sum
-    const float L = mine * l_run + (other.x == -INFINITY ? other.y : ex2f(other.x - M) * other.y);
-    const float f = L == 0.f ? 0.f : mine / L;
+    const float L = l_run + l_s[(half ^ 1) * kQ8RowTile];
+    const float f = L == 0.f ? 0.f : 1.f / L;
     if (active && nt > 0) {
-      float* dst = o_s + (half * kQ8RowTile + r_loc) * kORowG;
+      float* dst = reinterpret_cast<float*>(smem) + r_loc * kORowG + 64 * half;  // [128][kORowG]
 #pragma unroll 1
-      for (int c = 0; c < kDg; c += 32) {
+      for (int c = 0; c < 64; c += 32) {
         uint32_t oa[16], ob[16];
         tmem_ld16(tmem_o + c, oa);
         tmem_ld16(tmem_o + c + 16, ob);
@@ -540,7 +552,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
         }
       }
     }
-    if (half == 0) ml_s[2 * kQ8RowTile + r_loc] = make_float2(M, L);
+    if (half == 0) reinterpret_cast<float2*>(smem + Lay::kMl)[kQ8RowTile + r_loc] = make_float2(m, L);
   }
   tc_fence_before();
   __syncthreads();
@@ -553,28 +565,36 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
     // ---- the slices' rows: this CTA merges every a.cluster-th part of them ----
     if (a.cluster > 1) cluster_sync();  // every slice's rows are in its shared memory
     const int n = a.cluster, per = kQ8RowTile / n;
-    const uint32_t ml_at = smem_u32(smem + Lay::kMl) + 2 * kQ8RowTile * 8;
+    const uint32_t ml_at = smem_u32(smem + Lay::kMl) + kQ8RowTile * 8;
     for (int r = slice * per + warp; r < min(rows, (slice + 1) * per); r += kThreadsG / 32) {
-      float mm[8], w[8], M = -INFINITY, L = 0.f;
+      // every load before the first use, four slices at a time: a peer's
+      // memory is several hundred cycles away
+      float2 ml[8];
+      float M = -INFINITY, L = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        mm[i] = -INFINITY, w[i] = 0.f;
-        if (i < n) {
-          const float2 ml = ld_peer2(ml_at + r * 8, i);
-          mm[i] = ml.x, w[i] = ml.y;
-          M = fmaxf(M, ml.x);
-        }
-      }
+      for (int i = 0; i < 8; ++i) ml[i] = i < n ? ld_peer2(ml_at + r * 8, i) : make_float2(-INFINITY, 0.f);
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        w[i] *= mm[i] == -INFINITY ? 0.f : ex2f(mm[i] - M);
-        L += w[i];
-        if (i < n && w[i] != 0.f) {  // else that slice has no row there
-          const uint32_t at = sbase + (r * kORowG + 4 * lane) * 4;
-          const float4 x = ld_peer4(at, i), y = ld_peer4(at + kQ8RowTile * kORowG * 4, i);
-          acc.x += w[i] * (x.x + y.x), acc.y += w[i] * (x.y + y.y);
-          acc.z += w[i] * (x.z + y.z), acc.w += w[i] * (x.w + y.w);
+      for (int i0 = 0; i0 < 8; i0 += 4) {
+        if (i0 >= n) break;
+        const uint32_t at = sbase + (r * kORowG + 4 * lane) * 4;
+        float4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int from = min(i0 + i, n - 1);
+          x[i] = ld_peer4(at, from);
+        }
+        if (i0 == 0)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) M = fmaxf(M, ml[i].x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float w = (ml[i0 + i].x == -INFINITY ? 0.f : ex2f(ml[i0 + i].x - M)) * ml[i0 + i].y;
+          L += w;
+          if (w != 0.f) {  // else that slice has no row there
+            acc.x += w * x[i].x, acc.y += w * x[i].y;
+            acc.z += w * x[i].z, acc.w += w * x[i].w;
+          }
         }
       }
       const float inv = L == 0.f ? 0.f : 1.f / L;
@@ -583,16 +603,14 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
     if (a.cluster > 1) cluster_sync();  // no CTA leaves while its rows are read
     return;
   }
-  const float2* ml_s = reinterpret_cast<const float2*>(smem + Lay::kMl) + 2 * kQ8RowTile;
+  const float2* ml_s = reinterpret_cast<const float2*>(smem + Lay::kMl) + kQ8RowTile;
   if (tid < rows) __stcg(&a.pml[part * kQ8RowTile + tid], ml_s[tid]);
   if (nt > 0) {
     const float* o_s = reinterpret_cast<const float*>(smem);
     float4* dst = reinterpret_cast<float4*>(a.po + part * kQ8RowTile * kDg);
     for (int i = tid; i < rows * (kDg / 4); i += kThreadsG) {
       const float* at = o_s + i / (kDg / 4) * kORowG + i % (kDg / 4) * 4;
-      const float4 x = *reinterpret_cast<const float4*>(at);
-      const float4 y = *reinterpret_cast<const float4*>(at + kQ8RowTile * kORowG);
-      __stcg(dst + i, make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w));
+      __stcg(dst + i, *reinterpret_cast<const float4*>(at));
     }
   }
 }
