@@ -9,8 +9,11 @@
 // block that already holds tokens keeps its scale unless the new ones need a
 // larger one; then the CTA also moves the old codes to it.
 //
-// A CTA's block is (blockIdx.z's sequence, block blockIdx.x behind its first
-// new token) where the sequences' counts are alike.  Ragged counts would leave
+// Consecutive CTAs take the heads of one block: a token's row of heads is one
+// piece of memory, and heads read far apart in time cost DRAM pages.
+//
+// A CTA's block is (blockIdx.y's sequence, block blockIdx.x / units behind its
+// first new token) where the sequences' counts are alike.  Ragged counts would leave
 // many such CTAs without work, each a place on the GPU for the time of a load
 // (16 prompts of 517 .. 16384 tokens: half of them, 30 of 165 us); there the
 // touched blocks are numbered through, and each warp finds its CTA's block by
@@ -29,13 +32,15 @@ namespace {
 
 constexpr int kThreadsC = 256;
 
-// 8 elements of a row as floats; kept raw until they are used
+// 8 elements of a row as floats; kept raw until they are used.  New rows are
+// read once: marked so, they leave the L2 to the codes (16 fp32 prompts
+// 145 -> 122 us).
 template <bool F32>
 struct Raw8;
 template <>
 struct Raw8<false> {
   uint4 v;
-  __device__ __forceinline__ void load(const void* p) { v = __ldcg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void load(const void* p) { v = __ldcs(reinterpret_cast<const uint4*>(p)); }
   __device__ __forceinline__ void clear() { v = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ float get(int i) const {
     const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
@@ -46,8 +51,8 @@ template <>
 struct Raw8<true> {
   float4 a, b;
   __device__ __forceinline__ void load(const void* p) {
-    a = __ldcg(reinterpret_cast<const float4*>(p));
-    b = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+    a = __ldcs(reinterpret_cast<const float4*>(p));
+    b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
   }
   __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ float get(int i) const {
@@ -82,15 +87,17 @@ __global__ void __launch_bounds__(kThreadsC) cache_append_q8_kernel(const Q8Appe
   constexpr int kPer = kQ8Block * kPieces / kThreadsC;     // pieces a thread holds
   __shared__ uint32_t warp_max[kThreadsC / 32];
   const int tid = threadIdx.x;
-  const int h = blockIdx.y % a.Hkv, which = blockIdx.y / a.Hkv;
+  const int units = a.Hkv * (a.cache.codes[1] ? 2 : 1);  // (tensor, head)
+  const int unit = blockIdx.x % units;
+  const int h = unit % a.Hkv, which = unit / a.Hkv;
   pdl_trigger();
   pdl_wait();
   NewTokens nt;
-  int blk = blockIdx.x;  // block behind the sequence's first touched one
+  int blk = blockIdx.x / units;  // block behind the sequence's first touched one
   if (FLAT) {
     const int lane = tid & 31;
     // one CTA more than there can be blocks: it meets every sequence
-    const bool rep = blockIdx.y == 0 && blockIdx.x == gridDim.x - 1 && tid < 32;
+    const bool rep = blockIdx.x == gridDim.x - 1 && tid < 32;
     bool found = false;
     for (int base = 0; base < a.B && !found; base += 32) {
       int cnt = 0;
@@ -121,7 +128,7 @@ __global__ void __launch_bounds__(kThreadsC) cache_append_q8_kernel(const Q8Appe
     }
     if (!found) return;
   } else {
-    nt = new_tokens(a, blockIdx.z, tid == 0 && blockIdx.x == 0 && blockIdx.y == 0);
+    nt = new_tokens(a, blockIdx.y, tid == 0 && blockIdx.x == 0);
     if (blk >= nt.blocks()) return;
   }
   const Q8Seq& s = nt.s;
@@ -323,7 +330,7 @@ cudaError_t launch_cache_append_q8(const Q8AppendArgs& a, cudaStream_t stream) {
   const int64_t all = a.n_rows / kQ8Block + 2ll * a.B + 1;
   const int units = a.Hkv * (a.cache.codes[1] ? 2 : 1);
   const bool flat = blocks * a.B > all + all / 4;
-  const dim3 grid((unsigned)(flat ? all : blocks), units, flat ? 1 : a.B);
+  const dim3 grid((unsigned)((flat ? all : blocks) * units), flat ? 1 : a.B);
 #define SA_APPEND_CASE(DD)                                                                      \
   if (a.d == DD) {                                                                              \
     if (flat)                                                                                   \
