@@ -10,11 +10,11 @@
 // at least 64 rows, and its TMEM and commit chain costs more than a whole
 // pass here).
 //
-//   * One CTA of 8 warps per (sequence, KV head, 128 query rows, slice of the
-//     keys), two CTAs per SM.  The warps form RGW row groups of 8*NT rows
-//     times 8/RGW key groups; a key group walks its keys 16 at a time with a
-//     ring of three stages of its own (K and V codes and scales by cp.async,
-//     two passes ahead), so key groups never wait for one another.
+//   * One CTA of 8 warps per (sequence, KV head, slice of the keys), two CTAs
+//     per SM, for 8 or 16 query rows (more: attn_q8_group.cu).  Each warp walks
+//     keys of its own 16 at a time with a ring of three stages (K and V codes
+//     and scales by cp.async, two passes ahead): warps never wait for one
+//     another.
 //   * e4m3 codes become halves exactly (one conversion per two codes), in
 //     registers: S^T = K Q^T and O^T = V^T P^T are m16n8k16 f16 MMAs with fp32
 //     accumulators.  Queries are scaled per row by a power of two into the
@@ -38,9 +38,11 @@
 //     zero, whatever the cache holds there.
 //   * Partial results travel normalised: (m, l, o / l).  A weighted mean of V
 //     rows cannot leave V's own range, whatever the scales.
-//   * The slices of a (b, g) leave theirs in the workspace and count
-//     themselves on a counter in its header; the last one merges them and
-//     puts the counter back to zero.  Results do not depend on which is last.
+//   * The slices of a short (b, g) are a cluster of up to 8 CTAs and merge in
+//     shared memory.  Those of a long one leave their results in the workspace
+//     and count themselves on a counter in its header; the last one merges
+//     them and puts the counter back to zero.  Results do not depend on which
+//     is last.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -70,10 +72,10 @@ struct StageQ {
   float vs[kKeysQ];
 };
 
-template <int NT, int RGW>
+template <int NT>
 struct SmemQ {
-  static constexpr int kRows = RGW * 8 * NT;  // query rows of the CTA
-  static constexpr int kKW = kWarpsQ / RGW;   // key groups
+  static constexpr int kRows = 8 * NT;  // query rows of the CTA
+  static constexpr int kKW = kWarpsQ;   // key groups: the warps
   union {
     StageQ ring[kKW][kStagesQ];
     struct {
@@ -82,7 +84,7 @@ struct SmemQ {
     } w;
     float2 sml[q8_max_splits(kRows)][kRows];  // the merging CTA: each slice's (m, l), then (weight, -)
   };
-  uint4 q[RGW * NT][4][32];        // the query's B fragments: [8 rows][two k-steps][lane]
+  uint4 q[NT][4][32];        // the query's B fragments: [8 rows][two k-steps][lane]
   float rf[kRows];                 // per row: softmax scale * log2(e) / query scale
   float2 ml[kKW][kRows];           // each key group's (m, l)
   float2 ML[kRows];                // each row's (reference, sum of weights)
@@ -132,32 +134,29 @@ __device__ __forceinline__ float warp_key_max(float x) {
   return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
 }
 
-template <int NT, int RGW, bool PRECISE>
-__global__ void __launch_bounds__(kThreadsQ, 2) attn_q8_kernel(const Q8AttnArgs a, const int row_tiles) {
-  using Smem = SmemQ<NT, RGW>;
+template <int NT, bool PRECISE>
+__global__ void __launch_bounds__(kThreadsQ, 2) attn_q8_kernel(const Q8AttnArgs a) {
+  using Smem = SmemQ<NT>;
   constexpr int kRows = Smem::kRows, kKW = Smem::kKW;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gq = lane >> 2, tq = lane & 3;
-  const int rg = warp % RGW, kw = warp / RGW;  // row group, key group
-  const int gtid = rg * 32 + lane;             // thread of the key group
   const int slice = blockIdx.x % a.n_split;
-  const int unit = blockIdx.x / a.n_split;     // (b, g, row tile)
-  const int rt = unit % row_tiles;
-  const int g = unit / row_tiles % a.Hkv, b = unit / row_tiles / a.Hkv;
-  const int row_base = rt * kQ8RowTile;
+  const int unit = blockIdx.x / a.n_split;  // (b, g)
+  const int g = unit % a.Hkv, b = unit / a.Hkv;
   pdl_trigger();
   pdl_wait();
   const Q8Seq s = q8_seq(a.seq_off, a.seq_len, b, a.n_tokens, a.S_max);
   if (!s.ok && tid == 0 && slice == 0) report(a.status, kErrDevice, kKernAttnQ8, b, s.len, s.cap);
   const int n_keys = !s.ok ? 0 : a.idx ? a.k : s.len;  // entries, or tokens
-  const int e_beg = slice * a.chunk, e_end = min(n_keys, e_beg + a.chunk);
+  const int e_beg = (int)min((int64_t)n_keys, (int64_t)slice * a.chunk);
+  const int e_end = (int)min((int64_t)n_keys, (int64_t)e_beg + a.chunk);
   // slices of this unit that have keys (at least one): the others do nothing
-  const int n_live = max(1, (n_keys + a.chunk - 1) / a.chunk);
-  if (slice >= n_live) return;
+  const int n_live = max(1, (int)(((int64_t)n_keys + a.chunk - 1) / a.chunk));
+  if (slice >= n_live && !a.cluster) return;
   const int64_t row0 = s.off * a.Hkv + (int64_t)g * s.cap;
-  const int e_grp = e_beg + kw * kKeysQ;  // this group's passes: e_grp + p * kKW * 16
+  const int e_grp = e_beg + warp * kKeysQ;  // this group's passes: e_grp + p * kKW * 16
   const int n_pass = e_grp < e_end ? (e_end - e_grp + kKW * kKeysQ - 1) / (kKW * kKeysQ) : 0;
 
   // token of entry lane (< 16) of pass p, or -1; entries past the length are
@@ -170,40 +169,29 @@ __global__ void __launch_bounds__(kThreadsQ, 2) attn_q8_kernel(const Q8AttnArgs 
   // pass p's copies (t: its entries) into its stage; returns which entries are tokens
   auto issue = [&](int t, int p) -> uint32_t {
     if (t >= s.len) {
-      if (rg == 0 && g == 0 && rt == 0 && lane < 16)
+      if (g == 0 && lane < 16)
         report(a.status, kErrDevice, kKernAttnQ8, (int64_t)b * a.k + e_grp + p * (kKW * kKeysQ) + lane, t, s.len);
       t = -1;
     }
     if (p < n_pass) {
-      StageQ& st = sm.ring[kw][p % kStagesQ];
+      StageQ& st = sm.ring[warp][p % kStagesQ];
 #pragma unroll
-      for (int i = 0; i < (kKeysQ * 8 + RGW * 32 - 1) / (RGW * 32); ++i) {
-        const int j = gtid + i * (RGW * 32);  // 16-byte piece of the 16 rows
+      for (int i = 0; i < kKeysQ * 8 / 32; ++i) {
+        const int j = lane + i * 32;  // 16-byte piece of the 16 rows
         const int r = j >> 3, c = j & 7;
-        if (RGW * 32 <= kKeysQ * 8 || j < kKeysQ * 8) {
-          const int tr = __shfl_sync(0xffffffffu, t, r);
-          const int64_t at = (row0 + max(tr, 0)) * kDq + c * 16;
-          const uint32_t to = r * kDq + ((c ^ (r & 7)) << 4);
-          const uint32_t bytes = tr >= 0 ? 16u : 0u;
-          cp_async16(st.k + to, a.K + at, bytes);
-          cp_async16(st.v + to, a.V + at, bytes);
-        }
+        const int tr = __shfl_sync(0xffffffffu, t, r);
+        const int64_t at = (row0 + max(tr, 0)) * kDq + c * 16;
+        const uint32_t to = r * kDq + ((c ^ (r & 7)) << 4);
+        const uint32_t bytes = tr >= 0 ? 16u : 0u;
+        cp_async16(st.k + to, a.K + at, bytes);
+        cp_async16(st.v + to, a.V + at, bytes);
       }
-      if (rg == 0) {
-        const int64_t at = (row0 + max(t, 0)) / kQ8Block;
-        cp_async4(lane < 16 ? &st.ks[lane] : &st.vs[lane - 16], (lane < 16 ? a.Ks : a.Vs) + at, t >= 0 ? 4u : 0u);
-      }
+      const int64_t at = (row0 + max(t, 0)) / kQ8Block;
+      cp_async4(lane < 16 ? &st.ks[lane] : &st.vs[lane - 16], (lane < 16 ? a.Ks : a.Vs) + at, t >= 0 ? 4u : 0u);
     }
     cp_async_commit();
     return __ballot_sync(0xffffffffu, t >= 0);
   };
-  auto group_sync = [&]() {
-    if (RGW == 1)
-      __syncwarp();
-    else
-      asm volatile("bar.sync %0, %1;" ::"r"(kw + 1), "n"(RGW * 32) : "memory");
-  };
-
   int t_next = entry(0);
   const int t_second = entry(1);
   uint32_t seen = issue(t_next, 0);  // of the pass computed next, and of the one after it
@@ -212,7 +200,7 @@ __global__ void __launch_bounds__(kThreadsQ, 2) attn_q8_kernel(const Q8AttnArgs 
 
   // ---- the query rows as f16 fragments ----
   for (int r = warp; r < kRows; r += kWarpsQ) {
-    const int row = row_base + r;
+    const int row = r;
     uint2 v = make_uint2(0u, 0u);
     int64_t off = -1;
     if (row < a.R) {
@@ -240,8 +228,8 @@ __global__ void __launch_bounds__(kThreadsQ, 2) attn_q8_kernel(const Q8AttnArgs 
   float rf[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    rf[n][0] = sm.rf[(rg * NT + n) * 8 + 2 * tq];
-    rf[n][1] = sm.rf[(rg * NT + n) * 8 + 2 * tq + 1];
+    rf[n][0] = sm.rf[n * 8 + 2 * tq];
+    rf[n][1] = sm.rf[n * 8 + 2 * tq + 1];
   }
   float m_l[NT][2], m_o[NT][2], l_run[NT][2], o[NT][8][4];
 #pragma unroll
@@ -254,12 +242,12 @@ __global__ void __launch_bounds__(kThreadsQ, 2) attn_q8_kernel(const Q8AttnArgs 
 
   for (int p = 0; p < n_pass; ++p) {
     cp_async_wait<1>();
-    group_sync();  // pass p has landed; pass p - 1's stage is free
+    __syncwarp();  // pass p has landed; pass p - 1's stage is free
     const bool seen0 = seen >> gq & 1, seen1 = seen >> (gq + 8) & 1;
     seen = seen_after;
     seen_after = issue(t_next, p + 2);
     t_next = entry(p + 3);
-    const StageQ& st = sm.ring[kw][p % kStagesQ];
+    const StageQ& st = sm.ring[warp][p % kStagesQ];
     // ---- S^T = K Q^T: lane holds keys gq, gq + 8 at rows 2tq, 2tq + 1 ----
     float sc[NT][2][4];
 #pragma unroll
@@ -282,7 +270,7 @@ __global__ void __launch_bounds__(kThreadsQ, 2) attn_q8_kernel(const Q8AttnArgs 
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const uint4 q = sm.q[rg * NT + n][2 * i + j][lane];
+          const uint4 q = sm.q[n][2 * i + j][lane];
           mma_f16(sc[n][0], f[0][0], f[0][1], f[0][2], f[0][3], q.x, q.y);
           mma_f16(sc[n][1], f[1][0], f[1][1], f[1][2], f[1][3], q.z, q.w);
         }
@@ -388,19 +376,19 @@ __global__ void __launch_bounds__(kThreadsQ, 2) attn_q8_kernel(const Q8AttnArgs 
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int r = (rg * NT + n) * 8 + 2 * tq + e;
+      const int r = n * 8 + 2 * tq + e;
       const float inv = l_run[n][e] == 0.f ? 0.f : 1.f / l_run[n][e];  // a NaN sum stays one
       // 2^(m_o - m_l) in two halves: it may pass a float's range where the result does not
       const float half_up = m_l[n][e] == -INFINITY ? 0.f : ex2f(0.5f * (m_o[n][e] - m_l[n][e]));
       const auto value = [&](float x) { return x * inv * half_up * half_up; };
 #pragma unroll
       for (int c = 0; c < 8; ++c)
-        *reinterpret_cast<float2*>(&sm.w.o[kw][r][16 * c + 2 * gq]) =
+        *reinterpret_cast<float2*>(&sm.w.o[warp][r][16 * c + 2 * gq]) =
             make_float2(value(o[n][c][e]), value(o[n][c][2 + e]));
-      if (gq == 0) sm.ml[kw][r] = make_float2(m_l[n][e], l_run[n][e]);
+      if (gq == 0) sm.ml[warp][r] = make_float2(m_l[n][e], l_run[n][e]);
     }
   __syncthreads();
-  const int rows = min(kRows, a.R - row_base);
+  const int rows = min(kRows, a.R);
   if (tid < rows) {
     float M = -INFINITY, L = 0.f, f[kKW];
 #pragma unroll
@@ -438,10 +426,46 @@ __global__ void __launch_bounds__(kThreadsQ, 2) attn_q8_kernel(const Q8AttnArgs 
       acc.z += f * v.z;
       acc.w += f * v.w;
     }
-    if (n_live == 1)
+    if (a.n_split == 1 || n_live == 1 && !a.cluster)
       store_out(r, c, acc);
+    else if (a.cluster)
+      *reinterpret_cast<float4*>(&sm.w.o[0][r][c]) = acc;  // only this thread reads or writes it
     else
       __stcg(reinterpret_cast<float4*>(a.po + ((part0 + slice) * kRows + r) * kDq + c), acc);
+  }
+  if (a.n_split == 1) return;
+  if (a.cluster) {
+    // ---- the slices' rows: this CTA merges every n_split-th 16 bytes of them ----
+    cluster_sync();
+    for (int i = tid * a.n_split + slice; i < rows * (kDq / 4); i += kThreadsQ * a.n_split) {
+      const int r = i / (kDq / 4), c = i % (kDq / 4) * 4;
+      float2 ml[8];
+      float4 v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int from = min(j, a.n_split - 1);
+        ml[j] = ld_peer2(smem_u32(&sm.ML[r]), from);
+        v[j] = ld_peer4(smem_u32(&sm.w.o[0][r][c]), from);
+      }
+      float M = -INFINITY, L = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) M = fmaxf(M, ml[j].x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (j >= a.n_split) break;
+        const float f = (ml[j].x == -INFINITY ? 0.f : ex2f(ml[j].x - M)) * ml[j].y;
+        L += f;
+        acc.x += f * v[j].x;
+        acc.y += f * v[j].y;
+        acc.z += f * v[j].z;
+        acc.w += f * v[j].w;
+      }
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      store_out(r, c, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+    }
+    cluster_sync();  // no CTA leaves while its rows are read
+    return;
   }
   if (n_live == 1) return;
   if (tid < rows) __stcg(&a.pml[(part0 + slice) * kRows + tid], sm.ML[tid]);
@@ -490,10 +514,10 @@ __global__ void __launch_bounds__(kThreadsQ, 2) attn_q8_kernel(const Q8AttnArgs 
   if (tid == 0) a.cnt[unit] = 0;  // ready for the next launch on this workspace
 }
 
-template <int NT, int RGW>
+template <int NT>
 cudaError_t launch_nt(const Q8AttnArgs& a, const Q8AttnPlan& p, cudaStream_t stream) {
-  auto kern = a.out_f32 ? attn_q8_kernel<NT, RGW, true> : attn_q8_kernel<NT, RGW, false>;
-  const size_t smem = sizeof(SmemQ<NT, RGW>);
+  auto kern = a.out_f32 ? attn_q8_kernel<NT, true> : attn_q8_kernel<NT, false>;
+  const size_t smem = sizeof(SmemQ<NT>);
   cudaError_t e = ensure_smem(kern, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -501,39 +525,50 @@ cudaError_t launch_nt(const Q8AttnArgs& a, const Q8AttnPlan& p, cudaStream_t str
   cfg.blockDim = dim3(kThreadsQ);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1] = {pdl_attribute()};
+  cudaLaunchAttribute attr[2] = {pdl_attribute()};
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.cluster ? p.cluster : 1;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kern, a, p.row_tiles);
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, kern, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
-
-// rows a CTA takes: 8 (one n-tile), else 16 per row group, in 1, 2, 4 or 8 row groups
-int padded_rows(int R) { return R <= 8 ? 8 : R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 ? 64 : 128; }
 
 }  // namespace
 
 Q8AttnPlan plan_attn_q8(int R, int B, int Hkv, int64_t n_tokens, int S_max, int k, int sms, int max_counters) {
   Q8AttnPlan p;
-  p.row_tiles = (R + kQ8RowTile - 1) / kQ8RowTile;
-  p.rows = padded_rows(R);
-  p.units = B * Hkv * p.row_tiles;
   const int64_t n = k > 0 ? k : S_max;  // keys of the longest unit
   p.group = R > kQ8GroupRows;
+  p.row_tiles = p.group ? (R + kQ8RowTile - 1) / kQ8RowTile : 1;
+  p.units = B * Hkv * p.row_tiles;
   if (p.group) {
     plan_attn_q8_group(p, n, sms);
     return p;
   }
-  // keys a CTA takes per round of all its key groups
-  const int round = kKeysQ * (p.rows <= 16 ? kWarpsQ : kWarpsQ * 16 / p.rows);
-  const int64_t slots = 2ll * sms;      // CTAs the GPU holds at once
+  p.rows = R <= 8 ? 8 : 16;
+  constexpr int round = kKeysQ * kWarpsQ;  // keys a CTA takes per round of its warps
+  const int64_t slots = 2ll * sms;         // CTAs the GPU holds at once
   // Little work: one wave, at most one slice per slot.  Much work (from 2048
   // keys per slot): about four slices per slot, so that ragged sequences and
   // the last wave even out.
-  const int64_t keys = (k > 0 ? (int64_t)B * k : n_tokens) * Hkv * p.row_tiles;
+  const int64_t keys = (k > 0 ? (int64_t)B * k : n_tokens) * Hkv;
+  const bool little = keys < slots * 2048;
   const int64_t even = slots / p.units > 1 ? slots / p.units : 1;
-  int64_t chunk = keys < slots * 2048 ? (n + even - 1) / even : (keys + slots * 4 - 1) / (slots * 4);
-  if (p.units > max_counters) chunk = n;
+  int64_t chunk = little ? (n + even - 1) / even : (keys + slots * 4 - 1) / (slots * 4);
+  // a cluster merges faster than the workspace, at the price of at most four
+  // rounds where more slices would take fewer
+  p.cluster = 0;
+  const int64_t rounds = (n + round - 1) / round;
+  if (little && (even <= 8 || rounds <= 8 * 4)) {
+    const int64_t most = even < rounds ? even : rounds;
+    p.cluster = most >= 8 ? 8 : most >= 4 ? 4 : most >= 2 ? 2 : 1;
+    chunk = (n + p.cluster - 1) / p.cluster;
+  } else if (p.units > max_counters) {
+    chunk = n;
+  }
   const int most = q8_max_splits(p.rows);
   const int64_t least = (n + most - 1) / most;
   if (chunk < least) chunk = least;
@@ -541,9 +576,9 @@ Q8AttnPlan plan_attn_q8(int R, int B, int Hkv, int64_t n_tokens, int S_max, int 
   if (chunk < round) chunk = round;
   if (chunk > 0x7fffff00) chunk = 0x7fffff00;
   p.chunk = (int)chunk;
-  p.n_split = (int)((n + chunk - 1) / chunk);
+  p.n_split = p.cluster ? p.cluster : (int)((n + chunk - 1) / chunk);
   if (p.n_split < 1) p.n_split = 1;
-  p.parts = p.n_split;
+  p.parts = p.cluster ? 0 : p.n_split;
   return p;
 }
 
@@ -555,13 +590,7 @@ size_t attn_q8_scratch_bytes(const Q8AttnPlan& p) {
 
 cudaError_t launch_attn_q8(const Q8AttnArgs& a, const Q8AttnPlan& p, cudaStream_t stream) {
   if (p.group) return launch_attn_q8_group(a, p, stream);
-  switch (p.rows) {
-    case 8: return launch_nt<1, 1>(a, p, stream);
-    case 16: return launch_nt<2, 1>(a, p, stream);
-    case 32: return launch_nt<2, 2>(a, p, stream);
-    case 64: return launch_nt<2, 4>(a, p, stream);
-    default: return launch_nt<2, 8>(a, p, stream);
-  }
+  return p.rows == 8 ? launch_nt<1>(a, p, stream) : launch_nt<2>(a, p, stream);
 }
 
 }  // namespace sa

@@ -154,28 +154,6 @@ __device__ __forceinline__ void store_row(const Q8AttnArgs& a, int b, int g, int
         make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
 }
 
-// shared memory of the cluster's CTA `rank`, at this CTA's address
-__device__ __forceinline__ float4 ld_peer4(uint32_t addr, int rank) {
-  uint32_t at;
-  float4 v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(at)
-               : "memory");
-  return v;
-}
-__device__ __forceinline__ float2 ld_peer2(uint32_t addr, int rank) {
-  uint32_t at;
-  float2 v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
-  return v;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 template <bool PRECISE>
 __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8AttnArgs a, const int row_tiles) {
   using Lay = SmemG<PRECISE>;
@@ -226,7 +204,8 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
   const Q8Seq s = q8_seq(a.seq_off, a.seq_len, b, a.n_tokens, a.S_max);
   if (!s.ok && tid == 0 && slice == 0) report(a.status, kErrDevice, kKernAttnQ8, b, s.len, s.cap);
   const int n_keys = !s.ok ? 0 : a.idx ? a.k : s.len;  // entries, or tokens
-  const int e_beg = (int)min((int64_t)n_keys, (int64_t)slice * a.chunk), e_end = min(n_keys, e_beg + a.chunk);
+  const int e_beg = (int)min((int64_t)n_keys, (int64_t)slice * a.chunk), 
+            e_end = (int)min((int64_t)n_keys, (int64_t)e_beg + a.chunk);
   const int nt = (e_end - e_beg + kKeysG - 1) / kKeysG;
   // every role meets here once its first loads are on their way: barriers and TMEM are ready
   auto ready = [] {

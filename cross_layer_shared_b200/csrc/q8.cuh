@@ -73,6 +73,29 @@ __device__ __forceinline__ uint32_t q8_scale_bits(uint32_t amax_bits) {
   return (uint32_t)e << 23;
 }
 
+// ---- clusters ----
+// shared memory of the cluster's CTA `rank`, at this CTA's address
+__device__ __forceinline__ float4 ld_peer4(uint32_t addr, int rank) {
+  uint32_t at;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ld_peer2(uint32_t addr, int rank) {
+  uint32_t at;
+  float2 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // ---- cache_q8.cu ----
 struct Q8Cache {
   uint8_t* codes[2];  // K and V (or one tensor: [1] null)
@@ -148,7 +171,7 @@ struct Q8AttnArgs {
   void* O;
   int out_f32;
   int n_split, chunk;  // key slices of chunk keys (of the index entries, or of the tokens)
-  int cluster;         // attn_q8_group.cu: slices that merge as a cluster (0: through the workspace)
+  int cluster;         // slices that merge as a cluster (0: through the workspace)
   // n_split > 1: counters per (b, g, row tile), zero between launches, and
   // the slices' partials [unit][n_split][rows][128], (m, l) [unit][n_split][rows]
   uint32_t* cnt;
