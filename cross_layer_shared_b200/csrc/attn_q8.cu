@@ -147,6 +147,24 @@ __global__ void __launch_bounds__(kThreadsQ, 2) attn_q8_kernel(const Q8AttnArgs 
   const int g = unit % a.Hkv, b = unit / a.Hkv;
   pdl_trigger();
   pdl_wait();
+  // loads that need nothing of the sequence come first: the warp's query rows
+  // and the index entries of its first two passes
+  uint2 qv[NT];
+  int64_t q_off[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int row = warp + kWarpsQ * i;
+    q_off[i] = (((int64_t)(row / a.G) * a.B + b) * a.Hq + g * a.G + row % a.G) * kDq;
+    qv[i] = make_uint2(0u, 0u);
+    if (row < a.R) qv[i] = __ldcg(reinterpret_cast<const uint2*>(a.Q + q_off[i]) + lane);  // dims 4*lane ..
+  }
+  int t_first = -1, t_second = -1;
+  if (a.idx) {
+    const int64_t e = (int64_t)slice * a.chunk + warp * kKeysQ + (lane & 15);
+    const int64_t end = min((int64_t)a.k, (int64_t)(slice + 1) * a.chunk);
+    if (e < end) t_first = __ldcg(&a.idx[(int64_t)b * a.k + e]);
+    if (e + kKW * kKeysQ < end) t_second = __ldcg(&a.idx[(int64_t)b * a.k + e + kKW * kKeysQ]);
+  }
   const Q8Seq s = q8_seq(a.seq_off, a.seq_len, b, a.n_tokens, a.S_max);
   if (!s.ok && tid == 0 && slice == 0) report(a.status, kErrDevice, kKernAttnQ8, b, s.len, s.cap);
   const int n_keys = !s.ok ? 0 : a.idx ? a.k : s.len;  // entries, or tokens
@@ -192,22 +210,16 @@ __global__ void __launch_bounds__(kThreadsQ, 2) attn_q8_kernel(const Q8AttnArgs 
     cp_async_commit();
     return __ballot_sync(0xffffffffu, t >= 0);
   };
-  int t_next = entry(0);
-  const int t_second = entry(1);
-  uint32_t seen = issue(t_next, 0);  // of the pass computed next, and of the one after it
-  t_next = entry(2);
+  if (!a.idx || !s.ok) t_first = entry(0), t_second = entry(1);
+  uint32_t seen = issue(t_first, 0);  // of the pass computed next, and of the one after it
+  int t_next = entry(2);
   uint32_t seen_after = issue(t_second, 1);
 
   // ---- the query rows as f16 fragments ----
-  for (int r = warp; r < kRows; r += kWarpsQ) {
-    const int row = r;
-    uint2 v = make_uint2(0u, 0u);
-    int64_t off = -1;
-    if (row < a.R) {
-      const int h = g * a.G + row % a.G, l = row / a.G;
-      off = (((int64_t)l * a.B + b) * a.Hq + h) * kDq;
-      v = __ldcg(reinterpret_cast<const uint2*>(a.Q + off) + lane);  // dims 4*lane ..
-    }
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const int r = warp + kWarpsQ * i;
+    const uint2 v = qv[i];
     const float x0 = bf_lo(v.x), x1 = bf_hi(v.x), x2 = bf_lo(v.y), x3 = bf_hi(v.y);
     const float mx = fmaxf(fmaxf(fabsf(x0), fabsf(x1)), fmaxf(fabsf(x2), fabsf(x3)));
     const uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));
@@ -220,7 +232,7 @@ __global__ void __launch_bounds__(kThreadsQ, 2) attn_q8_kernel(const Q8AttnArgs 
     *dst = make_uint2(pack_half(x0 * up, x1 * up), pack_half(x2 * up, x3 * up));
     if (lane == 0) {
       sm.rf[r] = a.scale_log2 / up;
-      sm.out_off[r] = off;
+      sm.out_off[r] = q_off[i];
     }
   }
   __syncthreads();
