@@ -158,63 +158,71 @@ indexer_q8_kernel(const __grid_constant__ CUtensorMap tm_ki, const Q8IndexerArgs
   if (warp == 0) {
     // ---------------- key tiles ----------------
     if (lane == 0) {
-      int i = 0;
+      // (stages are counted, not divided for: a division takes as long as the rest of a turn)
+      int st = 0, issued = 0;
+      uint32_t phase = 1;  // of the stage's `empty` that frees it: passed at once on the first turn
       int64_t off = g_beg < g_end ? a.seq_off[b] : 0;
-      for (int g = g_beg; g < g_end; ++g, ++i) {
-        const int s = i % n_st;
+      for (int g = g_beg; g < g_end; ++g) {
         if (g >= prefix[b + 1]) {
           do ++b; while (g >= prefix[b + 1]);
           off = a.seq_off[b];
         }
-        if (!mbar_wait(&empty[s], ((i / n_st) & 1) ^ 1, kWaitLimitNs)) {
-          report(a.status, kErrTimeout, kKernIndexerQ8, blockIdx.x, 0, i);
+        if (!mbar_wait(&empty[st], phase, kWaitLimitNs)) {
+          report(a.status, kErrTimeout, kKernIndexerQ8, blockIdx.x, 0, g);
           break;
         }
         const int64_t row = off + (int64_t)(g - prefix[b]) * kTile;
-        mbar_arrive_expect_tx(&full[s], Lay::kStageBytes);
+        mbar_arrive_expect_tx(&full[st], Lay::kStageBytes);
 #pragma unroll
         for (int h = 0; h < NH; ++h)
-          tma_load_2d(ring + s * Lay::kStageBytes + h * kTile * 128, &tm_ki, &full[s], h * 128, (int)row);
+          tma_load_2d(ring + st * Lay::kStageBytes + h * kTile * 128, &tm_ki, &full[st], h * 128, (int)row);
+        ++issued;
+        if (++st == n_st) st = 0, phase ^= 1;
       }
       // drain: every load issued by this thread has landed before the CTA exits
-      for (int j = i - n_st; j < i; ++j)
-        if (j >= 0) mbar_wait(&full[j % n_st], (j / n_st) & 1, kWaitLimitNs);
+      for (int k = 0; k < n_st && k < issued; ++k) {
+        if (--st < 0) st = n_st - 1, phase ^= 1;
+        mbar_wait(&full[st], phase ^ 1, kWaitLimitNs);
+      }
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_e4m3(128, Lay::kCols);
-      int nseq = 0;
-      bool fresh = true;  // the next tile is its sequence's first here
+      const uint64_t a0 = umma_desc_sw128(smem_u32(ring), 16, 1024);
+      const uint64_t b0 = umma_desc_sw128(smem_u32(qbuf), 16, 1024);
+      int st = 0, nseq = 0;
+      uint32_t phase = 0;
+      int next = g_beg;  // first tile of the next sequence
       for (int g = g_beg, i = 0; g < g_end; ++g, ++i) {
-        const int s = i % n_st, c = i % kAcc;
-        while (g >= prefix[b + 1]) ++b, fresh = true;
+        const int c = i % kAcc;
         bool ok = true;
-        if (fresh) {
+        if (g == next) {
+          while (g >= prefix[b + 1]) ++b;
+          next = prefix[b + 1];
           if (nseq > 0) umma_commit(&qempty[(nseq - 1) & 1]);  // the last sequence's products
           ok = mbar_wait(&qfull[nseq & 1], (nseq >> 1) & 1, kWaitLimitNs);
-          fresh = false;
           ++nseq;
         }
-        if (!ok || !mbar_wait(&full[s], (i / n_st) & 1, kWaitLimitNs) ||
+        if (!ok || !mbar_wait(&full[st], phase, kWaitLimitNs) ||
             !mbar_wait(&tempty[c], ((i / kAcc) & 1) ^ 1, kWaitLimitNs)) {
           report(a.status, kErrTimeout, kKernIndexerQ8, blockIdx.x, 1, i);
           break;
         }
         tc_fence_after();
-        const uint32_t a_base = smem_u32(ring + s * Lay::kStageBytes);
-        const uint32_t b_base = smem_u32(qbuf + ((nseq - 1) & 1) * Lay::kQBytes);
+        // descriptors count 16-byte units
+        const uint64_t ad = a0 + (uint32_t)(st * (Lay::kStageBytes / 16));
+        const uint64_t bd = b0 + ((nseq - 1) & 1) * (uint32_t)(Lay::kQBytes / 16);
         const uint32_t d = tmem_base + c * Lay::kCols;
 #pragma unroll
         for (int k = 0; k < NH * 4; ++k) {
           if (k >= ksteps) break;
           const int h = k / 4, kk = k % 4;
-          const uint64_t ad = umma_desc_sw128(a_base + h * kTile * 128 + kk * 32, 16, 1024);
-          const uint64_t bd = umma_desc_sw128(b_base + h * Lay::kQHalf + kk * 32, 16, 1024);
-          umma_e4m3(d, ad, bd, idesc, k != 0);
+          umma_e4m3(d, ad + h * (kTile * 128 / 16) + kk * 2, bd + h * (Lay::kQHalf / 16) + kk * 2, idesc, k != 0);
         }
-        umma_commit(&empty[s]);
+        umma_commit(&empty[st]);
         umma_commit(&tfull[c]);
+        if (++st == n_st) st = 0, phase ^= 1;
       }
     }
   } else if (warp < 6) {
@@ -290,45 +298,51 @@ indexer_q8_kernel(const __grid_constant__ CUtensorMap tm_ki, const Q8IndexerArgs
       }
       uint8_t* hi = qbuf + (nseq & 1) * Lay::kQBytes;
       uint8_t* lo = hi + NPAD * 128;
-      for (int j = warp - 6; j < NPAD; j += 2) {
+      // four heads at a time, 8 lanes a head, 16 dims (one 16-byte chunk of codes) a lane
+      const int ch = lane & 7;
+#pragma unroll 2
+      for (int j = (warp - 6) * 4 + (lane >> 3); j < NPAD; j += 8) {
         // a padding head is zero: its columns add nothing
         const uint16_t* q = a.qI + ((int64_t)b * a.H_I + j) * a.d_I;
-        float x[NH][4];  // dims 4 * lane .. of each half
-        uint32_t mx = 0;
+        uint4 v[NH][2];
+        uint32_t mx = 0;  // largest |element|, as bf16 bits (ordered like the values)
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-          const int dim = h * 128 + lane * 4;
-          const uint2 v =
-              j < a.H_I && dim < a.d_I ? __ldcg(reinterpret_cast<const uint2*>(q + dim)) : make_uint2(0u, 0u);
-          x[h][0] = __uint_as_float(v.x << 16);
-          x[h][1] = __uint_as_float(v.x & 0xffff0000u);
-          x[h][2] = __uint_as_float(v.y << 16);
-          x[h][3] = __uint_as_float(v.y & 0xffff0000u);
+          const bool in = j < a.H_I && h * 128 + ch * 16 < a.d_I;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) mx = max(mx, __float_as_uint(x[h][u]) & 0x7fffffffu);
+          for (int u = 0; u < 2; ++u) {
+            v[h][u] = in ? __ldcg(reinterpret_cast<const uint4*>(q + h * 128 + ch * 16) + u) : make_uint4(0, 0, 0, 0);
+            mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(v[h][u].x & 0x7fff7fffu, v[h][u].y & 0x7fff7fffu),
+                                       __vmaxu2(v[h][u].z & 0x7fff7fffu, v[h][u].w & 0x7fff7fffu)));
+          }
         }
-        mx = __reduce_max_sync(0xffffffffu, mx);
-        const uint32_t sb = mx >= 0x7f800000u ? 0x3f800000u : q8_scale_bits(mx);
+        const float wj = j < a.H_I ? __ldcg(&a.w[(int64_t)b * a.H_I + j]) : 0.f;
+        mx = max(mx & 0xffffu, mx >> 16);
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const uint32_t sb = mx >= 0x7f80u ? 0x3f800000u : q8_scale_bits(mx << 16);
         const float inv = 1.f / __uint_as_float(sb);
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
-          if (h * 128 + lane * 4 >= a.d_I) continue;
-          float y[4];
+          const uint32_t w[8] = {v[h][0].x, v[h][0].y, v[h][0].z, v[h][0].w, v[h][1].x, v[h][1].y, v[h][1].z, v[h][1].w};
+          uint32_t ch_hi[4], ch_lo[4];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) y[u] = x[h][u] * inv;
-          const uint32_t ch = q8_from_float4(y[0], y[1], y[2], y[3]);
-          uint32_t p0, p1;
-          q8_to_half4(ch, p0, p1);
-          const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&p0));
-          const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&p1));
-          const uint32_t cl = q8_from_float4(y[0] - f0.x, y[1] - f0.y, y[2] - f1.x, y[3] - f1.y);
-          const uint32_t to = h * Lay::kQHalf + sw128_offset(j, lane >> 2) + (lane & 3) * 4;
-          *reinterpret_cast<uint32_t*>(hi + to) = ch;
-          *reinterpret_cast<uint32_t*>(lo + to) = cl;
+          for (int u = 0; u < 4; ++u) {
+            const float y0 = __uint_as_float(w[2 * u] << 16) * inv, y1 = __uint_as_float(w[2 * u] & 0xffff0000u) * inv;
+            const float y2 = __uint_as_float(w[2 * u + 1] << 16) * inv;
+            const float y3 = __uint_as_float(w[2 * u + 1] & 0xffff0000u) * inv;
+            ch_hi[u] = q8_from_float4(y0, y1, y2, y3);
+            uint32_t p0, p1;
+            q8_to_half4(ch_hi[u], p0, p1);
+            const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&p0));
+            const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&p1));
+            ch_lo[u] = q8_from_float4(y0 - f0.x, y1 - f0.y, y2 - f1.x, y3 - f1.y);
+          }
+          const uint32_t to = h * Lay::kQHalf + sw128_offset(j, ch);
+          *reinterpret_cast<uint4*>(hi + to) = make_uint4(ch_hi[0], ch_hi[1], ch_hi[2], ch_hi[3]);
+          *reinterpret_cast<uint4*>(lo + to) = make_uint4(ch_lo[0], ch_lo[1], ch_lo[2], ch_lo[3]);
         }
-        if (lane == 0)
-          wq[(nseq & 1) * NPAD + j] =
-              j < a.H_I ? __ldcg(&a.w[(int64_t)b * a.H_I + j]) * __uint_as_float(sb) : 0.f;
+        if (ch == 0) wq[(nseq & 1) * NPAD + j] = wj * __uint_as_float(sb);
       }
       fence_proxy_async_smem();
       __syncwarp();
