@@ -789,82 +789,27 @@ def block_union_prefill_noalloc(idx, q_pos, Q, K, V, block: int, scale: float, k
 Q8_BLOCK = 64
 
 
-_BF16, _F32, _I32, _I64, _U8, _E4M3 = (torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8,
-                                       torch.float8_e4m3fn)
-_current_gpu = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_native = None
 
 
-# A decode step's calls take a few microseconds on the GPU: these checks cost
-# one of each query per tensor, and sizes are compared as element counts.
-def _at(t: torch.Tensor, n: int, dtype, dev: int, name: str) -> int:
-    """Address of a contiguous tensor of n elements of dtype on GPU dev."""
-    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.numel() == n:
-        return t.data_ptr()
-    raise ValueError(f"{name} must be a contiguous tensor of {n} elements of {dtype} on GPU {dev}, not {t.dtype} "
-                     f"{tuple(t.shape)} on {t.device}")
+def _q8():
+    """The compiled marshalling of these calls (csrc/binding.cpp), bound to libsa."""
+    global _native
+    if _native is None:
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError(f"{_HERE}/_binding.so cannot be loaded ({e}): build it with"
+                               " `python -m cross_layer_shared_b200.build`") from e
+        lb = lib()
+        _binding.bind(*(ctypes.cast(fn, ctypes.c_void_p).value for fn in (
+            lb.sa_cache_append_q8, lb.sa_cache_read_q8, lb.sa_index_score_q8, lb.sa_decode_attn_q8)))
+        _native = _binding
+    return _native
 
 
-def _gpu(t: torch.Tensor, name: str) -> int:
-    """Index of t's GPU, which has to be the current one: the kernels run there."""
-    dev = t.get_device()
-    if dev < 0 or dev != _current_gpu():
-        raise ValueError(f"{name} must be on the current GPU, not on {t.device}")
-    return dev
-
-
-def _raise(code: int) -> None:
-    raise SAError(code, lib().sa_last_error().decode())
-
-
-def _out_code(t: torch.Tensor, name: str) -> int:
-    if t.dtype is _BF16:
-        return SA_BF16
-    if t.dtype is _F32:
-        return SA_F32
-    raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, not {t.dtype}")
-
-
-def _cache_q8(codes, scales, Hkv: int, d: int, dev: int, name: str):
-    """Checks one 8-bit cache; returns its addresses and token places."""
-    row = Hkv * d
-    n = codes.numel()
-    if Hkv < 1 or d < 1 or n % (Q8_BLOCK * row) or codes.shape[-1] != d:
-        raise ValueError(f"{name} must be [.., {d}] with a multiple of {Q8_BLOCK} token places of {Hkv} heads, not "
-                         f"{tuple(codes.shape)}")
-    return (_at(codes, n, _E4M3, dev, name), _at(scales, n // (d * Q8_BLOCK), _F32, dev, "scales of " + name),
-            n // row)
-
-
-def _pair_q8(K8, K_scale, V8, V_scale, Hkv: int, d: int, dev: int):
-    k, ks, n_tokens = _cache_q8(K8, K_scale, Hkv, d, dev, "K8")
-    if V8 is None and V_scale is None:
-        return k, ks, None, None, n_tokens
-    if V8 is None or V_scale is None:
-        raise ValueError("V8 and V_scale go together")
-    n = n_tokens * Hkv
-    return (k, ks, _at(V8, n * d, _E4M3, dev, "V8"), _at(V_scale, n // Q8_BLOCK, _F32, dev, "scales of V8"), n_tokens)
-
-
-def _new_rows(x: torch.Tensor, dev: int, name: str):
-    """Address of new tokens' rows [n, Hkv, d], each row of heads contiguous, and their stride in elements."""
-    n, Hkv, d = x.shape
-    s0, s1, s2 = x.stride()
-    if x.get_device() != dev or (s2 != 1 and d > 1 or s1 != d and Hkv > 1) and x.numel():
-        raise ValueError(f"{name} must be on GPU {dev} with each token's [Hkv, d] contiguous, not strides "
-                         f"{x.stride()} on {x.device}")
-    return x.data_ptr(), s0 if n > 1 else Hkv * d
-
-
-def _ws_q8(ws, need: int, dev: int):
-    """Address and size of the workspace (a new one of need bytes if there is none), and what keeps it alive."""
-    if ws is None:
-        ws = workspace(need, f"cuda:{dev}")
-    n = ws.numel()
-    return _at(ws, n, _U8, dev, "ws"), n, ws
-
-
-def _stream_on(stream, dev: int) -> int:
-    return _stream(stream) if stream is not None or _raw_stream is None else _raw_stream(dev)
+def _raw(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def cache_append_q8(new_K, new_V, K8, K_scale, V8, V_scale, seq_off, seq_len, new_off=None,
@@ -876,36 +821,12 @@ def cache_append_q8(new_K, new_V, K8, K_scale, V8, V_scale, seq_off, seq_len, ne
     [B+1]; None: one row per sequence) and land behind the tokens there:
     seq_len already counts them.  max_new: host bound of a sequence's new
     rows (default: n).  One tensor: new_V = V8 = V_scale = None."""
-    dev = _gpu(new_K, "new_K")
-    code = _out_code(new_K, "new_K")
-    k, sK = _new_rows(new_K, dev, "new_K")
-    n, Hkv, d = new_K.shape
-    B = seq_len.numel()
-    v, sV = None, 0
-    if new_V is not None:
-        if V8 is None:
-            raise ValueError("new_V and V8 go together")
-        if new_V.shape != new_K.shape or new_V.dtype is not new_K.dtype:
-            raise ValueError("new_K and new_V must have one shape and dtype")
-        v, sV = _new_rows(new_V, dev, "new_V")
-    elif V8 is not None:
-        raise ValueError("new_V and V8 go together")
-    K8p, Ksp, V8p, Vsp, n_tokens = _pair_q8(K8, K_scale, V8, V_scale, Hkv, d, dev)
-    off = None
-    if new_off is not None:
-        off = _at(new_off, B + 1, _I64, dev, "new_off")
-        if max_new is None:
-            max_new = n
-    elif n != B:
-        raise ValueError(f"without new_off every sequence gets one row: new_K must have {B} rows, not {n}")
-    else:
-        max_new = 1
-    wsp, wsn, ws = _ws_q8(ws, WS_HEADER_BYTES, dev)
-    code = lib().sa_cache_append_q8(k, sK, v, sV, code, n, off, max_new, K8p, Ksp, V8p, Vsp,
-                                    _at(seq_off, B + 1, _I64, dev, "seq_off"), _at(seq_len, B, _I32, dev, "seq_len"),
-                                    B, n_tokens, Hkv, d, wsp, wsn, _stream_on(stream, dev))
+    if ws is None:
+        ws = workspace(WS_HEADER_BYTES, K8.device)
+    code = (_native or _q8()).cache_append_q8(new_K, new_V, K8, K_scale, V8, V_scale, seq_off, seq_len, new_off,
+                                              max_new, ws, _raw(stream))
     if code:
-        _raise(code)
+        _check(code)
 
 
 def cache_read_q8(K8, K_scale, V8, V_scale, seq_off, seq_len, S_max: int, Hkv: int, idx=None, out_off=None,
@@ -916,65 +837,42 @@ def cache_read_q8(K8, K_scale, V8, V_scale, seq_off, seq_len, S_max: int, Hkv: i
     out_off[b]*Hkv of [n_out*Hkv, d] (out_off int64 [B+1], the running sum of
     seq_len; n_out its last value, or K's).  Returns (K, V), or K alone
     without V8."""
-    dev = _gpu(K8, "K8")
-    B, d = seq_len.numel(), K8.shape[-1]
-    K8p, Ksp, V8p, Vsp, n_tokens = _pair_q8(K8, K_scale, V8, V_scale, Hkv, d, dev)
-    if (idx is None) == (out_off is None):
-        raise ValueError("give either idx (picked rows) or out_off (whole sequences)")
-    if V is not None and V8 is None:
-        raise ValueError("V and V8 go together")
-    k, idxp, offp = 0, None, None
-    if idx is not None:
-        k = idx.shape[-1]
-        idxp = _at(idx, B * k, _I32, dev, "idx")
-        n_out, shape = 0, (B, Hkv, k, d)
-    else:
-        offp = _at(out_off, B + 1, _I64, dev, "out_off")
-        if n_out is None:
-            if K is None:
-                raise ValueError("give n_out, the token rows of the packed output, or K")
-            n_out = K.numel() // (Hkv * d)
-        shape = (n_out * Hkv, d)
-    if K is None:
-        K = torch.empty(shape, dtype=out_dtype, device=K8.device)
-    if V8 is not None and V is None:
-        V = torch.empty(shape, dtype=K.dtype, device=K8.device)
-    code = _out_code(K, "K")
-    if K.shape != shape:
-        raise ValueError(f"K must have shape {shape}, not {tuple(K.shape)}")
-    n = K.numel()
-    wsp, wsn, ws = _ws_q8(ws, WS_HEADER_BYTES, dev)
-    code = lib().sa_cache_read_q8(K8p, Ksp, V8p, Vsp, _at(seq_off, B + 1, _I64, dev, "seq_off"),
-                                  _at(seq_len, B, _I32, dev, "seq_len"), B, n_tokens, S_max, Hkv, d, idxp, k, offp,
-                                  n_out, _at(K, n, K.dtype, dev, "K"),
-                                  None if V is None else _at(V, n, K.dtype, dev, "V"), code, wsp, wsn,
-                                  _stream_on(stream, dev))
+    if K is None or V is None and V8 is not None or n_out is None and idx is None:
+        d = K8.shape[-1]
+        if idx is not None:
+            shape = (idx.shape[0], Hkv, idx.shape[1], d)
+        else:
+            if n_out is None:
+                if K is None:
+                    raise ValueError("give n_out, the token rows of the packed output, or K")
+                n_out = K.numel() // max(Hkv * d, 1)
+            shape = (n_out * Hkv, d)
+        if K is None:
+            K = torch.empty(shape, dtype=out_dtype, device=K8.device)
+        if V is None and V8 is not None:
+            V = torch.empty(shape, dtype=K.dtype, device=K8.device)
+    if ws is None:
+        ws = workspace(WS_HEADER_BYTES, K8.device)
+    code = (_native or _q8()).cache_read_q8(K8, K_scale, V8, V_scale, seq_off, seq_len, S_max, Hkv, idx, out_off,
+                                            n_out, K, V, ws, _raw(stream))
     if code:
-        _raise(code)
+        _check(code)
     return K if V8 is None else (K, V)
 
 
 def index_score_q8(qI, w, KI8, KI_scale, seq_off, seq_len, S_max: int, scores=None, ld: Optional[int] = None, ws=None,
                    stream=None) -> torch.Tensor:
     """index_score over an 8-bit key cache (sa_index_score_q8)."""
-    dev = _gpu(qI, "qI")
-    B, H_I, d_I = qI.shape
-    K8p, Ksp, n_tokens = _cache_q8(KI8, KI_scale, 1, d_I, dev, "KI8")
     if scores is None:
-        ld = int(ld if ld is not None else max(S_max, 1))
-        scores = torch.empty((B, ld), dtype=torch.float32, device=qI.device)
+        scores = torch.empty((qI.shape[0], int(ld if ld is not None else max(S_max, 1))), dtype=torch.float32,
+                             device=qI.device)
     elif ld is not None and ld != scores.shape[-1]:
         raise ValueError(f"ld={ld} does not match scores of {scores.shape[-1]} columns")
-    ld = scores.shape[-1]
-    if ld < S_max:
-        raise ValueError(f"scores must be [{B}, >= {S_max}], not {tuple(scores.shape)}")
-    wsp, wsn, ws = _ws_q8(ws, WS_HEADER_BYTES, dev)
-    code = lib().sa_index_score_q8(_at(qI, B * H_I * d_I, _BF16, dev, "qI"), _at(w, B * H_I, _F32, dev, "w"), K8p, Ksp,
-                                   _at(seq_off, B + 1, _I64, dev, "seq_off"), _at(seq_len, B, _I32, dev, "seq_len"),
-                                   B, n_tokens, S_max, H_I, d_I, _at(scores, B * ld, _F32, dev, "scores"), ld, wsp,
-                                   wsn, _stream_on(stream, dev))
+    if ws is None:
+        ws = workspace(WS_HEADER_BYTES, qI.device)
+    code = (_native or _q8()).index_score_q8(qI, w, KI8, KI_scale, seq_off, seq_len, S_max, scores, ws, _raw(stream))
     if code:
-        _raise(code)
+        _check(code)
     return scores
 
 
@@ -987,27 +885,16 @@ def decode_attn_q8(Q, K8, K_scale, V8, V_scale, seq_off, seq_len, S_max: int, Hk
     """Decode attention over 8-bit caches (sa_decode_attn_q8): Q bf16 [L, B,
     Hq, d] over the tokens of idx int32 [B, k] (shared by the L layers), or
     with idx None over every token of each sequence.  Returns O [L, B, Hq, d]."""
-    dev = _gpu(Q, "Q")
-    L, B, Hq, d = Q.shape
-    if V8 is None:
-        raise ValueError("V8 is missing")
-    K8p, Ksp, V8p, Vsp, n_tokens = _pair_q8(K8, K_scale, V8, V_scale, Hkv, d, dev)
-    k, idxp = 0, None
-    if idx is not None:
-        k = idx.shape[-1]
-        idxp = _at(idx, B * k, _I32, dev, "idx")
     if O is None:
-        O = torch.empty((L, B, Hq, d), dtype=out_dtype, device=Q.device)
-    code = _out_code(O, "O")
-    n = L * B * Hq * d
-    wsp, wsn, ws = _ws_q8(ws, 0 if ws is not None else
-                          decode_attn_q8_workspace_size(L, B, n_tokens, S_max, Hq, Hkv, d, k), dev)
-    code = lib().sa_decode_attn_q8(_at(Q, n, _BF16, dev, "Q"), K8p, Ksp, V8p, Vsp,
-                                   _at(seq_off, B + 1, _I64, dev, "seq_off"), _at(seq_len, B, _I32, dev, "seq_len"),
-                                   idxp, L, B, n_tokens, S_max, Hq, Hkv, d, k, scale, _at(O, n, O.dtype, dev, "O"),
-                                   code, wsp, wsn, _stream_on(stream, dev))
+        O = torch.empty(Q.shape, dtype=out_dtype, device=Q.device)
+    if ws is None:
+        L, B, Hq, d = Q.shape
+        ws = workspace(decode_attn_q8_workspace_size(L, B, K8.numel() // max(Hkv * d, 1), S_max, Hq, Hkv, d,
+                                                     0 if idx is None else idx.shape[-1]), Q.device)
+    code = (_native or _q8()).decode_attn_q8(Q, K8, K_scale, V8, V_scale, seq_off, seq_len, S_max, Hkv, scale, idx, O,
+                                             ws, _raw(stream))
     if code:
-        _raise(code)
+        _check(code)
     return O
 
 

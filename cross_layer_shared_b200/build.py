@@ -86,9 +86,36 @@ def build_timeline(force: bool = False) -> str:
     return TIMELINE_LIB
 
 
+BINDING = os.path.join(PKG, "_binding.so")
+
+
+def build_binding(force: bool = False) -> str:
+    """The marshalling of the 8-bit cache calls (csrc/binding.cpp): a Python
+    extension that reads torch's tensors; the entry points stay in libsa."""
+    src = os.path.join(CSRC, "binding.cpp")
+    if force or _stale(BINDING, [src, HEADER]):
+        import sysconfig
+
+        import torch
+        base = os.path.dirname(torch.__file__)
+        cuda = os.path.dirname(os.path.dirname(nvcc()))
+        inc = [sysconfig.get_paths()["include"], os.path.join(base, "include"),
+               os.path.join(base, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
+        lib = os.path.join(base, "lib")
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{i}" for i in inc), src, "-o",
+               BINDING + ".tmp", f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+        os.replace(BINDING + ".tmp", BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     _build_lib(LIB, BUILD, (), force)
+    build_binding(force)
     if force or _stale(SYNTH_LIB, [SYNTH_SRC]):
         cmd = [nvcc(), *NVFLAGS, "-shared", "-o", SYNTH_LIB + ".tmp", SYNTH_SRC]
         subprocess.check_call(cmd)
