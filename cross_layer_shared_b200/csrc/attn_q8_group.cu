@@ -412,8 +412,13 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
           const uint64_t neg2 = pair(neg_m, neg_m);
           uint64_t ls[2] = {0ull, 0ull};
           float top[2] = {-INFINITY, -INFINITY};
-          auto weights = [&](const uint32_t (&sv)[16], int c) {  // of keys 16c .. of this half
+          auto weights = [&](uint32_t (&sv)[16], int c) {  // of keys 16c .. of this half
             const uint32_t see = vis[c >> 1] >> (16 * (c & 1)) & 0xffffu;
+            if (see != 0xffffu) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (!(see >> e & 1u)) sv[e] = 0xff800000u;  // -inf
+            }
 #pragma unroll
             for (int q = 0; q < 2; ++q) {  // 8 keys: one 16-byte chunk of the row's P
               float2 y[4];
@@ -421,11 +426,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int at = 8 * q + 2 * i;
-                float2 x = unpair(fma2(pair(__uint_as_float(sv[at]), __uint_as_float(sv[at + 1])), scale2, neg2));
-                if (see != 0xffffu) {
-                  if (!(see >> at & 1u)) x.x = -INFINITY;
-                  if (!(see >> (at + 1) & 1u)) x.y = -INFINITY;
-                }
+                const float2 x = unpair(fma2(pair(__uint_as_float(sv[at]), __uint_as_float(sv[at + 1])), scale2, neg2));
                 top[i & 1] = fmaxf(fmaxf(x.x, x.y), top[i & 1]);
                 y[i] = make_float2(ex2f(x.x), ex2f(x.y));
                 h[i] = pack_bf16(y[i].x, y[i].y);
