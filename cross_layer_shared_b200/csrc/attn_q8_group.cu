@@ -21,9 +21,10 @@
 //     exponents for that); only then the row's sums move to a new m and the
 //     tile's weights are made again.  Both halves of a row keep one m: its two
 //     warps meet once a tile to agree on that.
-//   * bf16 outputs: weights are rounded to bf16, 8 bits, and l is the sum of
-//     the rounded ones, so that they add up to one.  fp32 outputs: three bf16
-//     parts (24 bits), for whose shared memory K has one stage instead of two.
+//   * l is a column of its own in the products: P times ones.  It is the sum of
+//     the weights as they were rounded, so that they add up to one, and costs
+//     the softmax nothing.  bf16 outputs: weights of 8 bits.  fp32 outputs: three bf16
+//     parts (24 bits), for whose shared memory K has one stage instead of three.
 //   * The key slices of 128 rows are a cluster of up to 8 CTAs: each leaves its
 //     rows' (m, l, o / l) in its shared memory and merges 128 / 8 rows of all
 //     of them.  More slices than that (few rows over a long context) go
@@ -61,7 +62,8 @@ struct SmemG {
   static constexpr int kK = kTileG;                      // after Q
   static constexpr int kV = kK + kStagesK * kTileG;
   static constexpr int kPlo = kV + kStagesV * kTileG;
-  static constexpr int kTok = kPlo + (kParts - 1) * kTileG;  // [2][128]: tokens of a tile's keys, -1 for none
+  static constexpr int kOnes = kPlo + (kParts - 1) * kTileG; // 16 x 128 ones, in two halves of 64 keys
+  static constexpr int kTok = kOnes + 4096;                  // [2][128]: tokens of a tile's keys, -1 for none
   static constexpr int kScale = kTok + 2 * kKeysG * 4;       // [2][128]: their (K, V) scales
   static constexpr int kSeen = kScale + 2 * kKeysG * 8;      // [4 tiles][4]: bit c of word w: key 32w + c is a token
   static constexpr int kMove = kSeen + 4 * 4 * 4;            // [2 tiles][8 warps]: a row of the warp leaves its range
@@ -90,11 +92,6 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
@@ -114,6 +111,25 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&v)[16]) {
                  "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
                :
                : "memory");
+}
+
+// One column of TMEM: 32 lanes, one value each.
+__device__ __forceinline__ float tmem_get(uint32_t at) {
+  uint32_t v;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(v) : "r"(at));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(v) : : "memory");
+  return __uint_as_float(v);
+}
+__device__ __forceinline__ void tmem_set(uint32_t at, float v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(at), "r"(__float_as_uint(v)) : "memory");
+}
+
+// Both phases, by every lane: no broadcast, and most often no wait.
+__device__ __forceinline__ bool warp_wait_both(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb) {
+  const bool ready = mbar_try_wait(a, pa) & mbar_try_wait(b, pb);
+  if (__all_sync(0xffffffffu, ready)) return true;
+  const bool ok = mbar_wait(a, pa, kWaitLimitNs) && mbar_wait(b, pb, kWaitLimitNs);
+  return __all_sync(0xffffffffu, ok);
 }
 
 __device__ __forceinline__ bool warp_wait_g(uint64_t* bar, uint32_t parity) {
@@ -304,6 +320,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
     const uint32_t tmem = *slot;
     if (lane == 0 && nt > 0) {
       constexpr uint32_t idesc_qk = umma_idesc_bf16(128, 128, false, false);
+      constexpr uint32_t idesc_l = umma_idesc_bf16(128, 16, false, false);
       constexpr uint32_t idesc_pv = umma_idesc_bf16(128, 128, false, true);
       auto pv = [&](int i) -> bool {
         if (!mbar_wait(&v_full[i % SV], (i / SV) & 1, kWaitLimitNs) ||
@@ -318,11 +335,13 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
           for (int kk = 0; kk < 4; ++kk) {  // keys 64h + 16kk ..
             const uint64_t vd = umma_desc_sw128(vst + h * 8192 + kk * 2048, kHalfG, 1024);
 #pragma unroll
-            for (int q = 0; q < Lay::kParts; ++q)
-              umma_bf16(tmem + 256,
-                        umma_desc_sw128((q == 0 ? pst : sbase + Lay::kPlo + (q - 1) * kTileG) + h * kHalfG + kk * 32, 16,
-                                        1024),
-                        vd, idesc_pv, (i | h | kk | q) != 0);
+            for (int q = 0; q < Lay::kParts; ++q) {
+              const uint64_t pd = umma_desc_sw128(
+                  (q == 0 ? pst : sbase + Lay::kPlo + (q - 1) * kTileG) + h * kHalfG + kk * 32, 16, 1024);
+              umma_bf16(tmem + 256, pd, vd, idesc_pv, (i | h | kk | q) != 0);
+              umma_bf16(tmem + 384, pd, umma_desc_sw128(sbase + Lay::kOnes + h * 2048 + kk * 32, 16, 1024), idesc_l,
+                        (i | h | kk | q) != 0);
+            }
           }
         umma_commit(&k_empty[i % SK]);
         umma_commit(&v_empty[i % SV]);
@@ -366,6 +385,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         sts16(sbase + qh * kHalfG + sw128_offset(r, i), qv[i].x, qv[i].y, qv[i].z, qv[i].w);
+      sts16(sbase + Lay::kOnes + 16 * tid, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
@@ -376,45 +396,43 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
     const bool active = row_base + (warp & 3) * 32 < a.R;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tmem_o = tmem + 256 + 64 * half + lane_base;  // this thread's columns of O
+    const uint32_t tmem_l = tmem + 384 + lane_base;
     volatile float* up_s = reinterpret_cast<volatile float*>(smem + Lay::kMl) + r_loc;  // [2][128], by half
     volatile uint32_t* move_s = reinterpret_cast<volatile uint32_t*>(smem + Lay::kMove);  // [2 tiles][8 warps]
     auto meet = [&] { asm volatile("bar.sync %0, 64;" ::"r"(3 + (warp & 3)) : "memory"); };  // the rows' two warps
     const uint64_t scale2 = pair(a.scale_log2, a.scale_log2);
-    float m = -INFINITY, l_run = 0.f;
+    float m = -INFINITY;
     // a wait that gave up: the warp goes on without waiting (on garbage, which
     // the status tells), so that no other warp waits for it at a barrier
     bool failed = false;
     for (int j = 0; j < nt; ++j) {
-      if (!failed) failed = !warp_wait_g(&s_full[j & 1], (j >> 1) & 1) || !warp_wait_g(&k_full[j % SK], (j / SK) & 1);
+      if (!failed) failed = !warp_wait_both(&s_full[j & 1], (j >> 1) & 1, &k_full[j % SK], (j / SK) & 1);
       tc_fence_after();
       const uint32_t* seen = seen_s + (j & 3) * 4;
       const uint32_t* vis = seen + 2 * half;
       if (active) {
         const uint32_t tmem_s = tmem + (j & 1) * 128 + 64 * half + lane_base;
+        uint32_t sa[16], sb[16];
+        tmem_ld16(tmem_s, sa);
+        const uint32_t vis0 = vis[0], vis1 = vis[1];
+        const bool all = (vis0 & vis1) == 0xffffffffu;
         const uint32_t pst = sbase + Lay::kK + j % SK * kTileG + half * kHalfG + r_loc * 128;
         const uint32_t plo = sbase + Lay::kPlo + half * kHalfG + r_loc * 128;
         if (__any_sync(0xffffffffu, m == -INFINITY) && (seen[0] | seen[1] | seen[2] | seen[3])) {
           // the rows' first key: their reference
           int c = 0;
           while (seen[c] == 0u) ++c;
-          uint32_t x;
-          asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];"
-                       : "=r"(x)
-                       : "r"(tmem_s - 64 * half + 32 * c + __ffs(seen[c]) - 1));
-          asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(x) : : "memory");
-          const float z = __uint_as_float(x) * a.scale_log2;
+          const float z = tmem_get(tmem_s - 64 * half + 32 * c + __ffs(seen[c]) - 1) * a.scale_log2;
           if (m == -INFINITY) m = fabsf(z) < 1e30f ? z : 0.f;
         }
-        float tile_l = 0.f;
 #pragma unroll 1
         for (int tries = 0; tries < 2; ++tries) {
           const float neg_m = m == -INFINITY ? 0.f : -m;
           const uint64_t neg2 = pair(neg_m, neg_m);
-          uint64_t ls[2] = {0ull, 0ull};
           float top[2] = {-INFINITY, -INFINITY};
           auto weights = [&](uint32_t (&sv)[16], int c) {  // of keys 16c .. of this half
-            const uint32_t see = vis[c >> 1] >> (16 * (c & 1)) & 0xffffu;
-            if (see != 0xffffu) {
+            if (!all) {
+              const uint32_t see = (c < 2 ? vis0 : vis1) >> (16 * (c & 1));
 #pragma unroll
               for (int e = 0; e < 16; ++e)
                 if (!(see >> e & 1u)) sv[e] = 0xff800000u;  // -inf
@@ -430,7 +448,6 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
                 top[i & 1] = fmaxf(fmaxf(x.x, x.y), top[i & 1]);
                 y[i] = make_float2(ex2f(x.x), ex2f(x.y));
                 h[i] = pack_bf16(y[i].x, y[i].y);
-                ls[i & 1] = add2(ls[i & 1], PRECISE ? pair(y[i].x, y[i].y) : pair(bf_lo(h[i]), bf_hi(h[i])));
               }
               const uint32_t off = (uint32_t)((2 * c + q) ^ (r_loc & 7)) << 4;
               sts16(pst + off, h[0], h[1], h[2], h[3]);
@@ -448,8 +465,7 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
             }
           };
           // a load of TMEM takes about as long as 16 keys' weights: one ahead
-          uint32_t sa[16], sb[16];
-          tmem_ld16(tmem_s, sa);
+          if (tries) tmem_ld16(tmem_s, sa);
           tmem_wait(sa);
           tmem_ld16(tmem_s + 16, sb);
           weights(sa, 0);
@@ -461,8 +477,6 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
           weights(sa, 2);
           tmem_wait(sb);
           weights(sb, 3);
-          const float2 l0 = unpair(ls[0]), l1 = unpair(ls[1]);
-          tile_l = (l0.x + l0.y) + (l1.x + l1.y);
           if (tries) break;
           const float mine = fmaxf(top[0], top[1]);
           const bool move = __any_sync(0xffffffffu, mine > kRangeG);
@@ -475,7 +489,6 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
           const float up = fmaxf(mine, up_s[(half ^ 1) * kQ8RowTile]);
           const float alpha = up > kRangeG ? ex2f(-up) : 1.f;
           if (up > kRangeG) m += up;
-          l_run *= alpha;
           if (j > 0) {
             // the last tile's PV must have landed before O is rescaled
             if (!failed) failed = !warp_wait_g(&o_done[(j - 1) & 3], ((j - 1) >> 2) & 1);
@@ -489,10 +502,10 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
               for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
               tmem_st16(tmem_o + c, ov);
             }
+            if (half == 0) tmem_set(tmem_l, tmem_get(tmem_l) * alpha);
             tmem_wait_st();
           }
         }
-        l_run += tile_l;
         fence_proxy_async_smem();
       }
       tc_fence_before();
@@ -507,10 +520,8 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
     if (failed && lane == 0) report(a.status, kErrTimeout, kKernAttnQ8, blockIdx.x, 2, warp);
     tc_fence_after();
     // every MMA is done (the barrier below): Q and the stages are free for the rows
-    float* l_s = reinterpret_cast<float*>(smem + Lay::kMl) + r_loc;
-    l_s[half * kQ8RowTile] = l_run;
     asm volatile("bar.sync 1, 256;" ::: "memory");
-    const float L = l_run + l_s[(half ^ 1) * kQ8RowTile];
+    const float L = active && nt > 0 ? tmem_get(tmem_l) : 0.f;
     const float f = L == 0.f ? 0.f : 1.f / L;
     if (active && nt > 0) {
       float* dst = reinterpret_cast<float*>(smem) + r_loc * kORowG + 64 * half;  // [128][kORowG]
