@@ -1267,7 +1267,9 @@ sa_status validate_q8(const void* K8, const float* Ks, const void* V8, const flo
     return fail(SA_ERR_INVALID_ARG, "%s: n_tokens=%lld must be a multiple of %d in [0, 2^31)", who,
                 (long long)n_tokens, sa::kQ8Block);
   if ((V8 == nullptr) != (Vs == nullptr)) return fail(SA_ERR_INVALID_ARG, "%s: V8 and V_scale go together", who);
-  if (!K8 || !Ks || !seq_off || !seq_len) return fail(SA_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  // (an empty cache or batch may have no memory)
+  if ((n_tokens > 0 && (!K8 || !Ks)) || (B > 0 && (!seq_off || !seq_len)))
+    return fail(SA_ERR_INVALID_ARG, "%s: NULL pointer", who);
   if (!aligned(K8, 16) || !aligned(V8, 16)) return fail(SA_ERR_INVALID_ARG, "%s: codes must be 16-byte aligned", who);
   if (!aligned(Ks, 4) || !aligned(Vs, 4)) return fail(SA_ERR_INVALID_ARG, "%s: scales must be 4-byte aligned", who);
   return SA_OK;
@@ -1286,7 +1288,8 @@ sa_status sa_cache_append_q8(const void* new_K, int64_t stride_K, const void* ne
   if (max_new < 0 || n_rows < 0) return fail(SA_ERR_INVALID_ARG, "%s: negative size", who);
   if (!new_off && (n_rows != B || max_new != 1))
     return fail(SA_ERR_INVALID_ARG, "%s: without new_off every sequence gets one row (n_rows = B, max_new = 1)", who);
-  if ((new_V == nullptr) != (V8 == nullptr)) return fail(SA_ERR_INVALID_ARG, "%s: new_V and V8 go together", who);
+  if ((new_V == nullptr) != (V8 == nullptr) && n_tokens > 0)
+    return fail(SA_ERR_INVALID_ARG, "%s: new_V and V8 go together", who);
   sa_status st = validate_q8(K8, K_scale, V8, V_scale, seq_off, seq_len, B, n_tokens, Hkv, who);
   if (st != SA_OK) return st;
   const int64_t piece = in_dtype == SA_BF16 ? 8 : 4;  // elements in 16 bytes
@@ -1329,7 +1332,8 @@ sa_status sa_cache_read_q8(const void* K8, const float* K_scale, const void* V8,
   if (S_max < 0 || k < 0 || n_out < 0) return fail(SA_ERR_INVALID_ARG, "%s: negative size", who);
   if ((idx == nullptr) == (out_off == nullptr))
     return fail(SA_ERR_INVALID_ARG, "%s: give either idx (picked rows) or out_off (whole sequences)", who);
-  if ((V == nullptr) != (V8 == nullptr)) return fail(SA_ERR_INVALID_ARG, "%s: V and V8 go together", who);
+  if ((V == nullptr) != (V8 == nullptr) && n_tokens > 0)
+    return fail(SA_ERR_INVALID_ARG, "%s: V and V8 go together", who);
   sa_status st = validate_q8(K8, K_scale, V8, V_scale, seq_off, seq_len, B, n_tokens, Hkv, who);
   if (st != SA_OK) return st;
   if ((st = check_ws(ws, ws_bytes, SA_WS_HEADER_BYTES, who)) != SA_OK) return st;
@@ -1367,7 +1371,7 @@ sa_status sa_index_score_q8(const void* qI, const float* w, const void* KI8, con
   if (st != SA_OK) return st;
   if (S_max < 0) return fail(SA_ERR_INVALID_ARG, "%s: S_max=%d < 0", who, S_max);
   if (ld < S_max) return fail(SA_ERR_INVALID_ARG, "%s: ld=%lld < S_max=%d", who, (long long)ld, S_max);
-  if ((st = validate_index(qI, w, KI8, H_I, d_I, who)) != SA_OK) return st;
+  if ((st = validate_index(qI, w, n_tokens > 0 ? KI8 : qI, H_I, d_I, who)) != SA_OK) return st;
   if (!scores) return fail(SA_ERR_INVALID_ARG, "%s: NULL pointer", who);
   if ((st = check_ws(ws, ws_bytes, SA_WS_HEADER_BYTES, who)) != SA_OK) return st;
   if (B == 0 || S_max == 0 || n_tokens == 0) return SA_OK;
@@ -1385,7 +1389,9 @@ sa_status sa_index_score_q8(const void* qI, const float* w, const void* KI8, con
 
 size_t sa_decode_attn_q8_workspace_size(int L_g, int B, int64_t n_tokens, int S_max, int Hq, int Hkv, int d, int k) {
   (void)d;
-  if (L_g < 1 || B < 1 || Hkv < 1 || Hq < Hkv || k < 0 || S_max < 0 || n_tokens < 0) return SA_WS_HEADER_BYTES;
+  if (L_g < 1 || L_g > 4096 || B < 1 || B > 4096 || Hkv < 1 || Hq < Hkv || Hq / Hkv > 128 || k < 0 || S_max < 0 ||
+      n_tokens < 0 || (int64_t)L_g * B * Hq >= (1ll << 31))
+    return SA_WS_HEADER_BYTES;  // the call itself refuses these
   return SA_WS_HEADER_BYTES + sa::attn_q8_scratch_bytes(sa::plan_attn_q8(L_g * (Hq / Hkv), B, Hkv, n_tokens, S_max, k,
                                                                          num_sms(), kSmallMaxCounters));
 }
@@ -1400,7 +1406,7 @@ sa_status sa_decode_attn_q8(const void* Q, const void* K8, const float* K_scale,
   if (S_max < 0) return fail(SA_ERR_INVALID_ARG, "%s: S_max=%d < 0", who, S_max);
   if (idx ? k < 1 : k != 0) return fail(SA_ERR_INVALID_ARG, "%s: k=%d (>= 1 with idx, 0 without)", who, k);
   if (d != 128) return fail(SA_ERR_UNSUPPORTED, "%s: d=%d (only 128 is built)", who, d);
-  if (!V8) return fail(SA_ERR_INVALID_ARG, "%s: NULL pointer", who);
+  if (!V8 && n_tokens > 0) return fail(SA_ERR_INVALID_ARG, "%s: NULL pointer", who);
   sa_status st = validate_q8(K8, K_scale, V8, V_scale, seq_off, seq_len, B, n_tokens, Hkv, who);
   if (st != SA_OK) return st;
   if (Hq % Hkv != 0) return fail(SA_ERR_INVALID_ARG, "%s: Hq=%d not a multiple of Hkv=%d", who, Hq, Hkv);
@@ -1409,17 +1415,18 @@ sa_status sa_decode_attn_q8(const void* Q, const void* K8, const float* K_scale,
   if (!Q || !O) return fail(SA_ERR_INVALID_ARG, "%s: NULL pointer", who);
   if (!aligned(Q, 16) || !aligned(O, 16)) return fail(SA_ERR_INVALID_ARG, "%s: Q and O must be 16-byte aligned", who);
   if (!(scale > 0.f && scale < INFINITY)) return fail(SA_ERR_INVALID_ARG, "%s: scale must be finite and > 0", who);
+  if ((int64_t)L_g * B * Hq >= (1ll << 31)) return fail(SA_ERR_UNSUPPORTED, "%s: too many rows", who);
   const int R = L_g * (Hq / Hkv);
   const sa::Q8AttnPlan p = sa::plan_attn_q8(R, B, Hkv, n_tokens, S_max, k, num_sms(), kSmallMaxCounters);
-  if ((int64_t)p.units * p.n_split >= (1ll << 31) || (int64_t)L_g * B * Hq >= (1ll << 31))
-    return fail(SA_ERR_UNSUPPORTED, "%s: too many rows", who);
+  if ((int64_t)p.units * p.n_split >= (1ll << 31)) return fail(SA_ERR_UNSUPPORTED, "%s: too many rows", who);
   if ((st = check_ws(ws, ws_bytes, SA_WS_HEADER_BYTES + sa::attn_q8_scratch_bytes(p), who)) != SA_OK) return st;
   sa::Q8AttnArgs a{};
   a.Q = reinterpret_cast<const uint16_t*>(Q);
-  a.K = reinterpret_cast<const uint8_t*>(K8);
-  a.Ks = K_scale;
-  a.V = reinterpret_cast<const uint8_t*>(V8);
-  a.Vs = V_scale;
+  // an empty cache: any address does for the copies of no bytes
+  a.K = reinterpret_cast<const uint8_t*>(n_tokens > 0 ? K8 : Q);
+  a.Ks = n_tokens > 0 ? K_scale : reinterpret_cast<const float*>(Q);
+  a.V = reinterpret_cast<const uint8_t*>(n_tokens > 0 ? V8 : Q);
+  a.Vs = n_tokens > 0 ? V_scale : reinterpret_cast<const float*>(Q);
   a.seq_off = seq_off;
   a.seq_len = seq_len;
   a.idx = idx;

@@ -236,7 +236,7 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor *idx = tensor_or_none(a[8], "idx"), *off = tensor_or_none(a[9], "out_off");
     const at::Tensor& K = tensor(a[11], "K");
     const at::Tensor* V = tensor_or_none(a[12], "V");
-    if (!V != !c.V) bad("V", " and V8 go together");
+    if (!V != (a[2] == Py_None)) bad("V", " and V8 go together");
     if (!idx == !off) bad("idx", " (picked rows) or out_off (whole sequences): give one of them");
     int64_t k = 0, n_out = 0, rows;
     const int32_t* idxp = nullptr;
@@ -303,7 +303,7 @@ PyObject* attn(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (L > INT32_MAX || Hq > INT32_MAX || d > INT32_MAX) bad("Q", " is too large");
     const int Hkv = int32_of(a[8], "Hkv");
     const Cache c = cache(a + 1, Hkv, d, dev, true);
-    if (!c.V) bad("V8", " is missing");
+    if (a[3] == Py_None) bad("V8", " is missing");
     const Seqs s = seqs(a[5], a[6], dev);
     if (s.B != B) bad("seq_len", " must have " + std::to_string(B) + " entries, not " + std::to_string(s.B));
     const int S_max = int32_of(a[7], "S_max");

@@ -346,7 +346,7 @@ cudaError_t launch_cache_append_q8(const Q8AppendArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_cache_read_q8(const Q8ReadArgs& a, cudaStream_t stream) {
   const int64_t pieces = (int64_t)(a.idx ? a.k : a.S_max) * (a.d / 16);
-  const dim3 grid((unsigned)((pieces + kReadPieces - 1) / kReadPieces), a.Hkv * (a.cache.codes[1] ? 2 : 1), a.B);
+  const dim3 grid((unsigned)((pieces + kReadPieces - 1) / kReadPieces), a.Hkv * (a.out[1] ? 2 : 1), a.B);
 #define SA_READ_CASE(DD)                                                                     \
   if (a.d == DD)                                                                             \
     return a.out_f32 ? launch_grid(cache_read_q8_kernel<true, DD>, a, grid, stream)          \

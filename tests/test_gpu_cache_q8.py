@@ -508,6 +508,286 @@ def test_what_lies_past_the_length_does_not_matter(dev):
     check_attn(Qt.float().numpy(), K, V, lens, None, 1, np.float32(0.1), O, F32)
 
 
+# ------------------------------------------------------------------ more than 16 query rows per KV head
+def group_case(dev, rng, lens, L, Hq, Hkv, k=0, pad=0.0, dt=BF16, scale=0.1, K=None, V=None, Qf=None, S=None):
+    if K is None:
+        K, V = filled(rng, lens, Hkv, 128, dev)
+    B, S = len(lens), max(lens) if S is None else S
+    Qt = torch.from_numpy((rng.standard_normal((L, B, Hq, 128)) if Qf is None else Qf).astype(np.float32)).to(BF16)
+    idx = picks(rng, lens, k, pad) if k else None
+    ws = sa.workspace(sa.decode_attn_q8_workspace_size(L, B, int(K.off[-1]), S, Hq, Hkv, 128, k), dev)
+    O = torch.full((L, B, Hq, 128), 7.0, dtype=dt, device=dev)
+    sa.decode_attn_q8(Qt.to(dev), *K.pair(), *V.pair(), i64(K.off, dev), i32(lens, dev), S, Hkv, scale,
+                      idx=None if idx is None else i32(idx, dev), O=O, ws=ws)
+    ok(ws)
+    check_attn(Qt.float().numpy(), K, V, lens, idx, Hkv, np.float32(scale), O, dt)
+    return O
+
+
+GROUP = {  # L, Hq, Hkv, lens, k, share of -1, dtype
+    "r17_one_token": (17, 1, 1, [1], 0, 0, BF16),
+    "r18_empty_sequences": (9, 4, 2, [0, 70, 0], 0, 0, F32),
+    "r24_k1": (6, 8, 2, [300, 5], 1, 0, F32),
+    "r24_one_tile_short": (6, 8, 2, [127, 3], 0, 0, BF16),
+    "r24_one_tile_long": (6, 8, 2, [129, 128], 0, 0, F32),
+    "r32_cluster2": (8, 4, 1, [250], 0, 0, BF16),
+    "r32_cluster4": (8, 4, 1, [400, 90], 0, 0, F32),
+    "r32_cluster8_ragged": (8, 4, 1, [1024, 1, 513], 0, 0, BF16),
+    "r20_k2048_padded": (5, 8, 2, [9000, 100], 2048, 0.4, F32),
+    "r96_k2048": (24, 4, 1, [5000, 2048, 2049], 2048, 0.05, BF16),
+    "r40_through_the_workspace": (10, 4, 1, [9000], 0, 0, F32),
+    "r40_through_the_workspace_bf16": (10, 4, 1, [8193, 4500], 0, 0, BF16),
+    "r129_two_row_tiles": (43, 3, 1, [300], 0, 0, F32),
+    "r256_many_units": (2, 256, 2, [130] * 40, 0, 0, BF16),
+}
+
+
+@pytest.mark.parametrize("name", list(GROUP))
+def test_attention_of_many_rows(name, dev):
+    L, Hq, Hkv, lens, k, pad, dt = GROUP[name]
+    rng = np.random.default_rng(100 + list(GROUP).index(name))
+    group_case(dev, rng, lens, L, Hq, Hkv, k, pad, dt)
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("rising", [1, -1])
+def test_attention_of_many_rows_moves_its_reference(rising, dt, dev):
+    """Logits that climb (or fall) by hundreds of units over a slice's tiles: sums and outputs move to new references,
+    rows on their own; one row's logits stay."""
+    rng = np.random.default_rng(7)
+    n, L, Hq = 1500, 8, 4
+    K, V = Cache([1536], 1, 128, dev), Cache([1536], 1, 128, dev)
+    k = rng.standard_normal((n, 1, 128))
+    k[:, 0, 0] = rising * np.linspace(-200, 200, n)
+    q8.append(K.codes[0], K.scales[0], k, n)
+    q8.append(V.codes[0], V.scales[0], rng.standard_normal((n, 1, 128)), n)
+    K.upload(), V.upload()
+    q = rng.standard_normal((L, 1, Hq, 128))
+    q[:, 0, :, 0] = 12 * rng.random((L, Hq))
+    q[0, 0, 0, 0] = 0
+    group_case(dev, rng, [n], L, Hq, 1, dt=dt, K=K, V=V, Qf=q)
+    group_case(dev, rng, [n], L, Hq, 1, k=900, dt=dt, K=K, V=V, Qf=q)
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+def test_attention_of_many_rows_far_apart_scales(dt, dev):
+    rng = np.random.default_rng(6)
+    lens = [700, 130]
+    K, V = filled(rng, lens, 1, 128, dev, spread=1.0, strong=[(0, 3, 40), (0, 5, -40), (0, 7, 20), (1, 0, -60)])
+    group_case(dev, rng, lens, 9, 2, 1, dt=dt, K=K, V=V, scale=0.25)
+    group_case(dev, rng, lens, 9, 2, 1, k=250, dt=dt, K=K, V=V, scale=0.25)
+
+
+def test_attention_of_many_rows_ignores_what_it_does_not_read(dev):
+    """NaN codes and scales past the length and in tokens the index does not name; a bad sequence; an entry past the
+    length."""
+    rng = np.random.default_rng(14)
+    lens = [70, 300]
+    K, V = filled(rng, lens, 1, 128, dev)
+    for C in (K, V):
+        for b, n in enumerate(lens):
+            C.codes[b][:, n:] = 127
+        C.codes[1][:, 5] = 127
+        C.upload()
+    Qt = torch.from_numpy(rng.standard_normal((6, 2, 4, 128)).astype(np.float32)).to(BF16)
+    idx = picks(rng, lens, 60)
+    idx[1][idx[1] == 5] = -1
+    args = (Qt.to(dev), *K.pair(), *V.pair(), i64(K.off, dev))
+    O = sa.decode_attn_q8(*args, i32(lens, dev), 300, 1, 0.1, idx=i32(idx, dev), out_dtype=F32)
+    check_attn(Qt.float().numpy(), K, V, lens, idx, 1, np.float32(0.1), O, F32)
+    idx[0, 7] = 70
+    ws = sa.workspace(1 << 16, dev)
+    O = sa.decode_attn_q8(*args, i32(lens, dev), 300, 1, 0.1, idx=i32(idx, dev), out_dtype=F32, ws=ws)
+    code, det = status(ws)
+    assert code == sa.SA_ERR_DEVICE and det == [12, 7, 70, 70]
+    check_attn(Qt.float().numpy(), K, V, lens, idx, 1, np.float32(0.1), O, F32)
+    sa.clear_status(ws)
+    O = sa.decode_attn_q8(*args, i32([129, 300], dev), 300, 1, 0.1, idx=i32(idx, dev), out_dtype=F32, ws=ws)
+    code, det = status(ws)
+    assert code == sa.SA_ERR_DEVICE and det[0] == 12 and det[1] == 0
+    assert (O[:, 0] == 0).all() and not (O[:, 1] == 0).any()
+
+
+def test_attention_of_many_rows_repeats_itself(dev):
+    """The same call twice, and on two streams at once, gives the same bits (no order of arrival enters)."""
+    rng = np.random.default_rng(15)
+    lens = [3000, 500]
+    K, V = filled(rng, lens, 2, 128, dev)
+    off, ln = i64(K.off, dev), i32(lens, dev)
+    Q = torch.from_numpy(rng.standard_normal((12, 2, 8, 128)).astype(np.float32)).to(dev).to(BF16)
+    idx = i32(picks(rng, lens, 700), dev)
+    one = sa.decode_attn_q8(Q, *K.pair(), *V.pair(), off, ln, 3000, 2, 0.1, idx=idx)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    wss = [sa.workspace(sa.WS_HEADER_BYTES, dev) for _ in streams]
+    outs = [[torch.zeros_like(one) for _ in range(6)] for _ in streams]
+    torch.cuda.synchronize()
+    for r in range(6):
+        for st, ws, o in zip(streams, wss, outs):
+            sa.decode_attn_q8(Q, *K.pair(), *V.pair(), off, ln, 3000, 2, 0.1, idx=idx, O=o[r], ws=ws, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(one, x) for o in outs for x in o)
+
+
+# ------------------------------------------------------------------ sizes at the ends
+def test_many_sequences(dev):
+    """4096 sequences of up to 64 tokens: one decode step's append, scores and attention."""
+    rng = np.random.default_rng(40)
+    B = 4096
+    lens = rng.integers(1, 64, B)
+    off = np.arange(B + 1) * 64
+    C = Cache([64 * B], 1, 64, dev)
+    C.off = off
+    x = torch.from_numpy(rng.standard_normal((int(lens.sum()), 1, 64)).astype(np.float32))
+    ws = sa.workspace(sa.WS_HEADER_BYTES, dev)
+    sa.cache_append_q8(x.to(dev), None, *C.pair(), None, None, i64(off, dev), i32(lens, dev),
+                       i64(np.concatenate([[0], np.cumsum(lens)]), dev), 64, ws=ws)
+    one = torch.from_numpy(rng.standard_normal((B, 1, 64)).astype(np.float32))
+    sa.cache_append_q8(one.to(dev), None, *C.pair(), None, None, i64(off, dev), i32(lens + 1, dev), ws=ws)
+    ok(ws)
+    q = torch.from_numpy(rng.standard_normal((B, 4, 64)).astype(np.float32)).to(BF16)
+    w = torch.ones((B, 4))
+    scores = sa.index_score_q8(q.to(dev), w.to(dev), *C.pair(), i64(off, dev), i32(lens + 1, dev), 64, ws=ws)
+    ok(ws)
+    got = scores.double().cpu().numpy()
+    at = np.concatenate([[0], np.cumsum(lens)])
+    for b in (0, 1, 777, 2048, B - 1):
+        codes, scales = np.zeros((1, 64, 64), np.uint8), np.zeros((1, 1))
+        q8.append(codes, scales, x.numpy()[at[b]:at[b + 1]], int(lens[b]))
+        q8.append(codes, scales, one.numpy()[b:b + 1], int(lens[b]) + 1)
+        k = q8.values(codes, scales)[0, :lens[b] + 1]
+        want, mag = q8.index_scores(q[b].float().numpy(), w[b].numpy(), k)
+        tol = 140 * 2 * U * mag + np.abs(k).sum(1) * np.abs(q[b].float().numpy()).max(1).sum() * 2.0 ** -17
+        assert (np.abs(got[b, :lens[b] + 1] - want) <= tol).all()
+
+
+def test_empty_cache_and_empty_batch(dev):
+    """No token place at all: rows of zeros, scores untouched, new tokens reported."""
+    e8 = lambda d: torch.empty((0, d), dtype=torch.float8_e4m3fn, device=dev)
+    s0 = torch.empty(0, device=dev)
+    off, ln = i64([0, 0, 0], dev), i32([0, 0], dev)
+    ws = sa.workspace(1 << 16, dev)
+    for L in (1, 9):
+        Q = torch.ones((L, 2, 2, 128), dtype=BF16, device=dev)
+        O = torch.full((L, 2, 2, 128), 7.0, device=dev)
+        sa.decode_attn_q8(Q, e8(128), s0, e8(128), s0, off, ln, 0, 1, 0.1, O=O, ws=ws)
+        assert (O == 0).all()
+        O.fill_(7)
+        sa.decode_attn_q8(Q, e8(128), s0, e8(128), s0, off, ln, 0, 1, 0.1, idx=i32([[-1] * 3] * 2, dev), O=O, ws=ws)
+        assert (O == 0).all()
+    ok(ws)
+    scores = torch.full((2, 4), 7.0, device=dev)
+    sa.index_score_q8(torch.ones((2, 4, 64), dtype=BF16, device=dev), torch.ones((2, 4), device=dev), e8(64), s0, off,
+                      ln, 4, scores=scores, ws=ws)
+    assert (scores == 7).all()
+    K, V = sa.cache_read_q8(e8(64), s0, e8(64), s0, off, ln, 0, 1, idx=i32([[-1], [-1]], dev), ws=ws)
+    assert (K == 0).all() and (V == 0).all()
+    ok(ws)
+    x = torch.ones((2, 1, 64), device=dev)
+    sa.cache_append_q8(x, x, e8(64), s0, e8(64), s0, off, i32([1, 1], dev), ws=ws)
+    assert status(ws)[0] == sa.SA_ERR_DEVICE
+    none = torch.empty((0, 1, 64), device=dev)
+    sa.cache_append_q8(none, None, e8(64), s0, None, None, i64([0], dev), i32([], dev))
+
+
+def test_offsets_past_32_bits(dev):
+    """The last sequence of a cache of more than 2^31 bytes of codes per tensor, and more than 2^32 with it."""
+    rng = np.random.default_rng(41)
+    Hkv, d, n, first = 8, 128, 300, (1 << 22) + 64 * 3
+    n_tokens = first + 320
+    K8, V8 = (torch.zeros((n_tokens * Hkv, d), dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn) for _ in range(2))
+    Ks, Vs = (torch.zeros(n_tokens * Hkv // 64, device=dev) for _ in range(2))
+    off, ln = i64([0, first, n_tokens], dev), i32([0, n], dev)
+    (tk, xk), (tv, xv) = (rows(rng, n, Hkv, d, BF16) for _ in range(2))
+    ws = sa.workspace(1 << 20, dev)
+    sa.cache_append_q8(tk.to(dev), tv.to(dev), K8, Ks, V8, Vs, off, ln, i64([0, 0, n], dev), ws=ws)
+    C = []
+    for x in (xk, xv):
+        c = Cache([320], Hkv, d, dev, fill=0)
+        q8.append(c.codes[0], c.scales[0], x, n)
+        C.append(c)
+    K, V = sa.cache_read_q8(K8, Ks, V8, Vs, off, ln, n, Hkv, out_off=i64([0, 0, n], dev), n_out=n, out_dtype=F32, ws=ws)
+    for got, c in ((K, C[0]), (V, C[1])):
+        assert np.array_equal(got.double().cpu().numpy().reshape(Hkv, n, d), q8.values(c.codes[0], c.scales[0])[:, :n])
+    for L, G in ((1, 4), (6, 4)):
+        Q = torch.from_numpy(rng.standard_normal((L, 2, Hkv * G, d)).astype(np.float32)).to(BF16)
+        O = sa.decode_attn_q8(Q.to(dev), K8, Ks, V8, Vs, off, ln, n, Hkv, 0.1, out_dtype=F32, ws=ws)
+        assert (O[:, 0] == 0).all()
+        check_attn(Q[:, 1:].float().numpy(), *C, [n], None, Hkv, np.float32(0.1), O[:, 1:], F32)
+    ok(ws)
+    # the same memory as one indexer-key cache of 2^25 tokens and more
+    kI = K8.view(-1, d)
+    scores = torch.zeros((1, 64), device=dev)
+    at = (n_tokens * Hkv // 64 - 5 * Hkv) * 64  # head 0 of the last sequence
+    q = torch.from_numpy(rng.standard_normal((1, 16, d)).astype(np.float32)).to(BF16)
+    w = torch.ones((1, 16))
+    sa.index_score_q8(q.to(dev), w.to(dev), kI, Ks, i64([at, at + 64], dev), i32([64], dev), 64, scores=scores, ws=ws)
+    ok(ws)
+    k = q8.values(C[0].codes[0], C[0].scales[0])[0, :64]
+    want, mag = q8.index_scores(q[0].float().numpy(), w[0].numpy(), k)
+    tol = 300 * 2 * U * mag + np.abs(k).sum(1) * np.abs(q[0].float().numpy()).max(1).sum() * 2.0 ** -17
+    assert (np.abs(scores[0].double().cpu().numpy() - want) <= tol).all()
+
+
+def test_read_into_outputs_between_two_sectors(dev):
+    """Outputs that are 16- but not 32-byte aligned."""
+    rng = np.random.default_rng(42)
+    K, V = filled(rng, [100], 2, 128, dev)
+    for dt, skip in ((BF16, 8), (F32, 4)):
+        base = [torch.full((100 * 2 * 128 + 2 * skip,), 7.0, dtype=dt, device=dev) for _ in range(2)]
+        out = [t[skip:-skip].view(200, 128) for t in base]
+        assert out[0].data_ptr() % 32 == 16
+        sa.cache_read_q8(*K.pair(), *V.pair(), i64(K.off, dev), i32([100], dev), 100, 2, out_off=i64([0, 100], dev),
+                         K=out[0], V=out[1])
+        for o, t, C in zip(out, base, (K, V)):
+            assert np.array_equal(o.double().cpu().numpy().reshape(2, 100, 128), q8.values(C.codes[0], C.scales[0])[:, :100])
+            assert (t[:skip] == 7).all() and (t[-skip:] == 7).all()
+
+
+def test_calls_refuse_wrong_tensors(dev):
+    rng = np.random.default_rng(43)
+    K, V = filled(rng, [100], 2, 128, dev)
+    off, ln = i64(K.off, dev), i32([100], dev)
+    Q = torch.zeros((1, 1, 4, 128), dtype=BF16, device=dev)
+    good = dict(Q=Q, K8=K.c8, K_scale=K.s, V8=V.c8, V_scale=V.s, seq_off=off, seq_len=ln, S_max=100, Hkv=2, scale=0.1)
+    sa.decode_attn_q8(**good)
+    for name, wrong in (("Q", Q.float()), ("Q", Q.cpu()), ("Q", Q[0]), ("Q", Q.expand(2, 1, 4, 128)), ("K8", K.c8.view(torch.uint8)),
+                        ("K8", K.c8[:-64]), ("K8", K.c8.cpu()), ("V8", V.c8[:128]), ("V8", None), ("V_scale", None),
+                        ("K_scale", K.s.double()), ("K_scale", K.s[:-1]), ("seq_off", off.int()), ("seq_off", off[:1]),
+                        ("seq_len", ln.long()), ("Hkv", 0), ("Hkv", 3), ("S_max", 1 << 40), ("scale", "x"),
+                        ("idx", torch.zeros((1, 4), device=dev)), ("idx", torch.zeros((2, 4), dtype=torch.int32, device=dev)),
+                        ("idx", torch.zeros(4, dtype=torch.int32, device=dev)), ("O", Q.half()), ("O", Q[..., :64]),
+                        ("O", torch.zeros((1, 1, 4, 256), dtype=BF16, device=dev)[..., ::2]),
+                        ("ws", torch.zeros(4096, device=dev)), ("ws", torch.zeros(4096, dtype=torch.uint8))):
+        with pytest.raises(ValueError):
+            sa.decode_attn_q8(**dict(good, **{name: wrong}))
+    with pytest.raises(sa.SAError, match="WORKSPACE"):
+        sa.decode_attn_q8(**dict(good, ws=torch.zeros(256, dtype=torch.uint8, device=dev)))
+    x = torch.zeros((1, 2, 128), device=dev)
+    good = dict(new_K=x, new_V=x, K8=K.c8, K_scale=K.s, V8=V.c8, V_scale=V.s, seq_off=off, seq_len=ln)
+    for name, wrong in (("new_K", x.half()), ("new_K", x.transpose(1, 2)), ("new_K", x[:, :1]), ("new_V", None), ("V8", None),
+                        ("new_V", x.to(BF16)), ("new_K", x.cpu()), ("new_K", torch.zeros((2, 2, 128), device=dev)),
+                        ("new_off", i32([0, 1], dev)), ("new_off", i64([0, 1, 1], dev)), ("K8", None)):
+        with pytest.raises((ValueError, AttributeError)):
+            sa.cache_append_q8(**dict(good, **{name: wrong}))
+    idx = i32([[1, 2]], dev)
+    good = dict(K8=K.c8, K_scale=K.s, V8=V.c8, V_scale=V.s, seq_off=off, seq_len=ln, S_max=100, Hkv=2, idx=idx)
+    out = torch.zeros((1, 2, 2, 128), device=dev)
+    for name, wrong in (("idx", None), ("out_off", i64([0, 100], dev)), ("K", out[:, :1]), ("K", out.half()), ("K", out.cpu()),
+                        ("V", out), ("Hkv", 5)):
+        with pytest.raises(ValueError):
+            sa.cache_read_q8(**dict(good, **{name: wrong}))
+    k1, _ = filled(rng, [100], 1, 64, dev)
+    q = torch.zeros((1, 4, 64), dtype=BF16, device=dev)
+    good = dict(qI=q, w=torch.zeros((1, 4), device=dev), KI8=k1.c8, KI_scale=k1.s, seq_off=i64(k1.off, dev), seq_len=ln, S_max=100)
+    for name, wrong in (("qI", q.float()), ("qI", q[0]), ("w", torch.zeros((1, 3), device=dev)), ("KI8", k1.c8.view(-1, 128)),
+                        ("scores", torch.zeros((1, 99), device=dev)), ("scores", torch.zeros(100, device=dev)),
+                        ("scores", torch.zeros((1, 100), dtype=BF16, device=dev)), ("ld", 50),
+                        ("seq_len", i32([100, 1], dev))):
+        with pytest.raises((ValueError, sa.SAError)):
+            sa.index_score_q8(**dict(good, **{name: wrong}))
+
+
 # ------------------------------------------------------------------ together
 def step_case(dev, B=3, L=5, Hq=8, Hkv=2, H=4, d_I=64, k=128, lens=(300, 700, 1500)):
     rng = np.random.default_rng(20)
@@ -554,10 +834,11 @@ def plain_step(c, lens, dev):
     return O
 
 
-def test_decode_steps_with_append_eager_and_captured(dev):
+@pytest.mark.parametrize("Hq", [8, 16])  # 12 and 8 query rows per KV head and group of layers, or 24 and 16
+def test_decode_steps_with_append_eager_and_captured(Hq, dev):
     """Two steps: one eager, one replayed from a graph captured on another stream; new tokens, lengths and queries
     change in place between them."""
-    c = step_case(dev)
+    c = step_case(dev, Hq=Hq)
     ln = i32([n + 1 for n in c["lens"]], dev)
     n_tokens = int(c["off"][-1])
     ws = sa.workspace(sa.decode_step_q8_workspace_size(c["L"], c["B"], n_tokens, c["S"], c["Hq"], c["Hkv"], 128, c["k"]), dev)
