@@ -10,8 +10,8 @@
 // at least 64 rows, and its TMEM and commit chain costs more than a whole
 // pass here).
 //
-//   * One CTA of 8 warps per (sequence, KV head, slice of the keys), two CTAs
-//     per SM, for 8 or 16 query rows (more: attn_q8_group.cu).  Each warp walks
+//   * One CTA of 8 warps per (sequence, KV head, 8 or 16 query rows, slice of
+//     the keys), two CTAs per SM (much work of many rows: attn_q8_group.cu).  Each warp walks
 //     keys of its own 16 at a time with a ring of three stages (K and V codes
 //     and scales by cp.async, two passes ahead): warps never wait for one
 //     another.
@@ -38,11 +38,11 @@
 //     zero, whatever the cache holds there.
 //   * Partial results travel normalised: (m, l, o / l).  A weighted mean of V
 //     rows cannot leave V's own range, whatever the scales.
-//   * The slices of a short (b, g) are a cluster of up to 8 CTAs and merge in
-//     shared memory.  Those of a long one leave their results in the workspace
-//     and count themselves on a counter in its header; the last one merges
-//     them and puts the counter back to zero.  Results do not depend on which
-//     is last.
+//   * The slices of a short unit are a cluster of up to 8 CTAs and merge in
+//     shared memory.  More slices leave their results (a cluster's, or with
+//     much work each slice's) in the workspace and count themselves on a
+//     counter in its header; the last one merges them and puts the counter back
+//     to zero.  Results do not depend on which is last.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -135,7 +135,7 @@ __device__ __forceinline__ float warp_key_max(float x) {
 }
 
 template <int NT, bool PRECISE>
-__global__ void __launch_bounds__(kThreadsQ, 2) attn_q8_kernel(const Q8AttnArgs a) {
+__global__ void __launch_bounds__(kThreadsQ, 2) attn_q8_kernel(const Q8AttnArgs a, const int row_tiles) {
   using Smem = SmemQ<NT>;
   constexpr int kRows = Smem::kRows, kKW = Smem::kKW;
   extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -143,8 +143,10 @@ __global__ void __launch_bounds__(kThreadsQ, 2) attn_q8_kernel(const Q8AttnArgs 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gq = lane >> 2, tq = lane & 3;
   const int slice = blockIdx.x % a.n_split;
-  const int unit = blockIdx.x / a.n_split;  // (b, g)
-  const int g = unit % a.Hkv, b = unit / a.Hkv;
+  const int unit = blockIdx.x / a.n_split;  // (b, g, row tile)
+  const int rt = unit % row_tiles;
+  const int g = unit / row_tiles % a.Hkv, b = unit / row_tiles / a.Hkv;
+  const int row_base = rt * kRows;
   pdl_trigger();
   pdl_wait();
   // loads that need nothing of the sequence come first: the warp's query rows
@@ -153,8 +155,9 @@ __global__ void __launch_bounds__(kThreadsQ, 2) attn_q8_kernel(const Q8AttnArgs 
   int64_t q_off[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
-    const int row = warp + kWarpsQ * i;
-    q_off[i] = (((int64_t)(row / a.G) * a.B + b) * a.Hq + g * a.G + row % a.G) * kDq;
+    const int row = row_base + warp + kWarpsQ * i;
+    const int l = row < a.G ? 0 : row / a.G;
+    q_off[i] = (((int64_t)l * a.B + b) * a.Hq + g * a.G + row - l * a.G) * kDq;
     qv[i] = make_uint2(0u, 0u);
     if (row < a.R) qv[i] = __ldcg(reinterpret_cast<const uint2*>(a.Q + q_off[i]) + lane);  // dims 4*lane ..
   }
@@ -187,7 +190,7 @@ __global__ void __launch_bounds__(kThreadsQ, 2) attn_q8_kernel(const Q8AttnArgs 
   // pass p's copies (t: its entries) into its stage; returns which entries are tokens
   auto issue = [&](int t, int p) -> uint32_t {
     if (t >= s.len) {
-      if (g == 0 && lane < 16)
+      if (g == 0 && rt == 0 && lane < 16)
         report(a.status, kErrDevice, kKernAttnQ8, (int64_t)b * a.k + e_grp + p * (kKW * kKeysQ) + lane, t, s.len);
       t = -1;
     }
@@ -400,7 +403,7 @@ __global__ void __launch_bounds__(kThreadsQ, 2) attn_q8_kernel(const Q8AttnArgs 
       if (gq == 0) sm.ml[warp][r] = make_float2(m_l[n][e], l_run[n][e]);
     }
   __syncthreads();
-  const int rows = min(kRows, a.R);
+  const int rows = min(kRows, a.R - row_base);
   if (tid < rows) {
     float M = -INFINITY, L = 0.f, f[kKW];
 #pragma unroll
@@ -425,7 +428,18 @@ __global__ void __launch_bounds__(kThreadsQ, 2) attn_q8_kernel(const Q8AttnArgs 
       *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.O) + off) =
           make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
   };
-  const int64_t part0 = (int64_t)unit * a.n_split;
+  // what meets in the workspace: slices, or clusters of them (all of which
+  // count there, with keys or without); a single one is the result
+  const int sh = a.cluster ? 31 - __clz(a.cluster) : 0;
+  const int n_parts = a.cluster ? a.n_split >> sh : n_live;
+  const int part = slice >> sh;
+  const int64_t part0 = (int64_t)unit * (a.cluster ? n_parts : a.n_split);
+  auto store_part = [&](int r, int c, float4 v) {
+    if (n_parts == 1)
+      store_out(r, c, v);
+    else
+      __stcg(reinterpret_cast<float4*>(a.po + ((part0 + part) * kRows + r) * kDq + c), v);
+  };
   for (int i = tid; i < rows * (kDq / 4); i += kThreadsQ) {
     const int r = i / (kDq / 4), c = i % (kDq / 4) * 4;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -438,24 +452,22 @@ __global__ void __launch_bounds__(kThreadsQ, 2) attn_q8_kernel(const Q8AttnArgs 
       acc.z += f * v.z;
       acc.w += f * v.w;
     }
-    if (a.n_split == 1 || n_live == 1 && !a.cluster)
-      store_out(r, c, acc);
-    else if (a.cluster)
+    if (a.cluster > 1)
       *reinterpret_cast<float4*>(&sm.w.o[0][r][c]) = acc;  // only this thread reads or writes it
     else
-      __stcg(reinterpret_cast<float4*>(a.po + ((part0 + slice) * kRows + r) * kDq + c), acc);
+      store_part(r, c, acc);
   }
-  if (a.n_split == 1) return;
-  if (a.cluster) {
-    // ---- the slices' rows: this CTA merges every n_split-th 16 bytes of them ----
+  if (a.cluster > 1) {
+    // ---- the cluster's rows: this CTA merges every a.cluster-th 16 bytes of them ----
     cluster_sync();
-    for (int i = tid * a.n_split + slice; i < rows * (kDq / 4); i += kThreadsQ * a.n_split) {
+    const int n = a.cluster;
+    for (int i = tid * n + (slice & (n - 1)); i < rows * (kDq / 4); i += kThreadsQ * n) {
       const int r = i / (kDq / 4), c = i % (kDq / 4) * 4;
       float2 ml[8];
       float4 v[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int from = min(j, a.n_split - 1);
+        const int from = min(j, n - 1);
         ml[j] = ld_peer2(smem_u32(&sm.ML[r]), from);
         v[j] = ld_peer4(smem_u32(&sm.w.o[0][r][c]), from);
       }
@@ -465,7 +477,7 @@ __global__ void __launch_bounds__(kThreadsQ, 2) attn_q8_kernel(const Q8AttnArgs 
       for (int j = 0; j < 8; ++j) M = fmaxf(M, ml[j].x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        if (j >= a.n_split) break;
+        if (j >= n) break;
         const float f = (ml[j].x == -INFINITY ? 0.f : ex2f(ml[j].x - M)) * ml[j].y;
         L += f;
         acc.x += f * v[j].x;
@@ -474,29 +486,30 @@ __global__ void __launch_bounds__(kThreadsQ, 2) attn_q8_kernel(const Q8AttnArgs 
         acc.w += f * v[j].w;
       }
       const float inv = L == 0.f ? 0.f : 1.f / L;
-      store_out(r, c, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+      store_part(r, c, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+      if (c == 0 && n_parts > 1) __stcg(&a.pml[(part0 + part) * kRows + r], make_float2(M, L));
     }
-    cluster_sync();  // no CTA leaves while its rows are read
-    return;
+    cluster_sync();  // no CTA goes on while its rows are read
+  } else if (tid < rows && n_parts > 1) {
+    __stcg(&a.pml[(part0 + part) * kRows + tid], sm.ML[tid]);
   }
-  if (n_live == 1) return;
-  if (tid < rows) __stcg(&a.pml[(part0 + slice) * kRows + tid], sm.ML[tid]);
-  // ---- count this slice; the last one merges ----
+  if (n_parts == 1) return;
+  // ---- count this CTA; the last one merges ----
   __threadfence();
   __syncthreads();
-  if (tid == 0) sm.last = atomicAdd(&a.cnt[unit], 1u) == (unsigned)(n_live - 1);
+  if (tid == 0) sm.last = atomicAdd(&a.cnt[unit], 1u) == (unsigned)((a.cluster ? a.n_split : n_live) - 1);
   __syncthreads();
   if (!sm.last) return;
   __threadfence();
-  for (int i = tid; i < n_live * kRows; i += kThreadsQ)
+  for (int i = tid; i < n_parts * kRows; i += kThreadsQ)
     if (i % kRows < rows) (&sm.sml[0][0])[i] = __ldcg(&a.pml[part0 * kRows + i]);
   __syncthreads();
   for (int r = warp; r < rows; r += kWarpsQ) {
     float M = -INFINITY, L = 0.f;
-    for (int i = lane; i < n_live; i += 32) M = fmaxf(M, sm.sml[i][r].x);
+    for (int i = lane; i < n_parts; i += 32) M = fmaxf(M, sm.sml[i][r].x);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-    for (int i = lane; i < n_live; i += 32) {
+    for (int i = lane; i < n_parts; i += 32) {
       const float2 ml = sm.sml[i][r];
       const float f = (ml.x == -INFINITY ? 0.f : ex2f(ml.x - M)) * ml.y;
       sm.sml[i][r].x = f;
@@ -512,7 +525,7 @@ __global__ void __launch_bounds__(kThreadsQ, 2) attn_q8_kernel(const Q8AttnArgs 
     const float* src = a.po + (part0 * kRows + r) * kDq + c;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-    for (int j = 0; j < n_live; ++j) {
+    for (int j = 0; j < n_parts; ++j) {
       const float4 v = __ldcg(reinterpret_cast<const float4*>(src + (int64_t)j * kRows * kDq));
       const float f = sm.sml[j][r].x;
       acc.x += f * v.x;
@@ -544,53 +557,92 @@ cudaError_t launch_nt(const Q8AttnArgs& a, const Q8AttnPlan& p, cudaStream_t str
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, kern, a);
+  e = cudaLaunchKernelEx(&cfg, kern, a, p.row_tiles);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
+namespace {
+constexpr int kRound = kKeysQ * kWarpsQ;  // keys a CTA takes per round of its warps
+
+// How a unit's keys are split where all slices run at once: in one cluster of
+// 1, 2, 4 or 8 CTAs, in several of 8, or one by one through the workspace.
+// What counts is the rounds a CTA takes (about a microsecond each) and what
+// the merge adds to them: a cluster's barrier and reads 1, a meeting in the
+// workspace 2, and one CTA reading s partial results s / 16 more.
+// (One head of 1500, 2500 and 4000 tokens: one cluster of 8 takes 7.2, 8.2 and
+// 9.2 us, more slices through the workspace 9.1, 9.4 and 9.6.)
+struct Split {
+  int cluster = 1;       // CTAs of a cluster (0: none, every slice on its own)
+  int64_t slices = 1;
+  double cost = 1e30;
+  int64_t rounds = 0;    // of a CTA
+};
+
+Split split_once(int64_t units, int64_t rounds, int sms, bool counters) {
+  // whole clusters that run at once, two CTAs an SM: a GPC holds no parts of
+  // one (33 of 8 and 71 of 4 CTAs on 148 SMs)
+  const int64_t fit[4] = {2ll * sms, sms, 8ll * sms / 17, 2ll * sms / 9};
+  Split best;
+  auto offer = [&](int cluster, int64_t slices, double merge) {
+    const int64_t r = (rounds + slices - 1) / slices;
+    if ((double)r + merge < best.cost) best = {cluster, slices, (double)r + merge, r};
+  };
+  offer(1, 1, 0);
+  for (int i = 1; i < 4; ++i)
+    if (units <= fit[i] && rounds > 1 << (i - 1)) offer(1 << i, 1ll << i, 1);
+  if (counters) {
+    int64_t m = fit[3] / units;
+    if (m > (rounds + 7) / 8) m = (rounds + 7) / 8;
+    if (m > 1) offer(8, 8 * m, 3 + m / 16.0);
+    int64_t one = fit[0] / units;
+    if (one > rounds) one = rounds;
+    if (one > 1) offer(0, one, 2 + one / 16.0);
+  }
+  return best;
+}
+}  // namespace
+
 Q8AttnPlan plan_attn_q8(int R, int B, int Hkv, int64_t n_tokens, int S_max, int k, int sms, int max_counters) {
   Q8AttnPlan p;
   const int64_t n = k > 0 ? k : S_max;  // keys of the longest unit
-  p.group = R > kQ8GroupRows;
-  p.row_tiles = p.group ? (R + kQ8RowTile - 1) / kQ8RowTile : 1;
+  const int64_t rounds = n > kRound ? (n + kRound - 1) / kRound : 1;
+  const int64_t slots = 2ll * sms;      // CTAs the GPU holds at once
+  // More than 16 rows: 16 a CTA, K and V read again for every 16, where all
+  // CTAs run at once for two rounds at most; else tiles of 128 rows.  (20 rows
+  // of 16 heads, 2048 keys: 13.8 and 22.7 us; 96 rows of 8 heads: 16.8 in
+  // three rounds and 14.1.)
+  const int64_t tiles16 = (R + 15) / 16;
+  const int64_t units16 = B * (int64_t)Hkv * tiles16;
+  Split split = split_once(units16, rounds, sms, units16 <= max_counters);
+  p.group = R > 16 && (units16 > slots || split.rounds > 2);
+  p.row_tiles = p.group ? (R + kQ8RowTile - 1) / kQ8RowTile : (int)tiles16;
   p.units = B * Hkv * p.row_tiles;
   if (p.group) {
     plan_attn_q8_group(p, n, sms);
     return p;
   }
   p.rows = R <= 8 ? 8 : 16;
-  constexpr int round = kKeysQ * kWarpsQ;  // keys a CTA takes per round of its warps
-  const int64_t slots = 2ll * sms;         // CTAs the GPU holds at once
-  // Little work: one wave, at most one slice per slot.  Much work (from 2048
-  // keys per slot): about four slices per slot, so that ragged sequences and
-  // the last wave even out.
-  const int64_t keys = (k > 0 ? (int64_t)B * k : n_tokens) * Hkv;
-  const bool little = keys < slots * 2048;
-  const int64_t even = slots / p.units > 1 ? slots / p.units : 1;
-  int64_t chunk = little ? (n + even - 1) / even : (keys + slots * 4 - 1) / (slots * 4);
-  // a cluster merges faster than the workspace, at the price of at most four
-  // rounds where more slices would take fewer
-  p.cluster = 0;
-  const int64_t rounds = (n + round - 1) / round;
-  if (little && (even <= 8 || rounds <= 8 * 4)) {
-    const int64_t most = even < rounds ? even : rounds;
-    p.cluster = most >= 8 ? 8 : most >= 4 ? 4 : most >= 2 ? 2 : 1;
-    chunk = (n + p.cluster - 1) / p.cluster;
-  } else if (p.units > max_counters) {
-    chunk = n;
+  // Much work (from 2048 keys per slot): about four slices per slot, so that
+  // ragged sequences and the last wave even out.
+  const int64_t keys = (k > 0 ? (int64_t)B * k : n_tokens) * Hkv * p.row_tiles;
+  int64_t chunk = (n + split.slices - 1) / split.slices;
+  if (keys >= slots * 2048) {
+    split.cluster = 0;
+    chunk = p.units > max_counters ? n : (keys + slots * 4 - 1) / (slots * 4);
   }
   const int most = q8_max_splits(p.rows);
-  const int64_t least = (n + most - 1) / most;
+  const int64_t least = split.cluster ? 0 : (n + most - 1) / most;
   if (chunk < least) chunk = least;
-  chunk = (chunk + round - 1) / round * round;
-  if (chunk < round) chunk = round;
+  chunk = (chunk + kRound - 1) / kRound * kRound;
+  if (chunk < kRound) chunk = kRound;
   if (chunk > 0x7fffff00) chunk = 0x7fffff00;
   p.chunk = (int)chunk;
-  p.n_split = p.cluster ? p.cluster : (int)((n + chunk - 1) / chunk);
+  p.cluster = split.cluster;
+  p.n_split = p.cluster ? (int)split.slices : (int)((n + chunk - 1) / chunk);
   if (p.n_split < 1) p.n_split = 1;
-  p.parts = p.cluster ? 0 : p.n_split;
+  p.parts = p.cluster ? p.n_split / p.cluster : p.n_split;
   return p;
 }
 

@@ -152,7 +152,7 @@ struct Q8IndexerArgs {
 cudaError_t launch_indexer_q8(const Q8IndexerArgs& a, const CUtensorMap& tm_ki, int num_sms, cudaStream_t stream);
 
 // ---- attn_q8.cu ----
-constexpr int kQ8RowTile = 128;   // query rows of a (b, g) one CTA takes at most
+constexpr int kQ8RowTile = 128;     // query rows of a CTA of attn_q8_group.cu
 // key slices of a unit: their (m, l) of `rows` rows fit the merging CTA's shared memory
 __host__ __device__ constexpr int q8_max_splits(int rows) { return 8192 / rows < 256 ? 8192 / rows : 256; }
 struct Q8AttnArgs {
@@ -188,8 +188,7 @@ Q8AttnPlan plan_attn_q8(int R, int B, int Hkv, int64_t n_tokens, int S_max, int 
 size_t attn_q8_scratch_bytes(const Q8AttnPlan& p);
 cudaError_t launch_attn_q8(const Q8AttnArgs& a, const Q8AttnPlan& p, cudaStream_t stream);
 
-// ---- attn_q8_group.cu: more than kQ8GroupRows query rows per (b, g) ----
-constexpr int kQ8GroupRows = 16;
+// ---- attn_q8_group.cu ----
 void plan_attn_q8_group(Q8AttnPlan& p, int64_t n, int sms);
 cudaError_t launch_attn_q8_group(const Q8AttnArgs& a, const Q8AttnPlan& p, cudaStream_t stream);
 

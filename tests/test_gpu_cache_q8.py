@@ -539,6 +539,18 @@ GROUP = {  # L, Hq, Hkv, lens, k, share of -1, dtype
     "r40_through_the_workspace_bf16": (10, 4, 1, [8193, 4500], 0, 0, BF16),
     "r129_two_row_tiles": (43, 3, 1, [300], 0, 0, F32),
     "r256_many_units": (2, 256, 2, [130] * 40, 0, 0, BF16),
+    # units enough that tiles of 128 rows are taken, in clusters of 8, 4, 2 and 1
+    "r128_cluster8": (16, 16, 2, [3000, 2000], 0, 0, F32),
+    "r96_cluster4": (24, 32, 8, [700, 1, 300], 0, 0, BF16),
+    "r96_cluster4_f32_k": (24, 32, 8, [2500, 800, 2100, 500], 600, 0.1, F32),
+    "r24_cluster2": (3, 64, 8, [1100, 5, 600, 0, 129, 128, 900, 64], 0, 0, BF16),
+    "r130_two_row_tiles_cluster1": (13, 80, 8, [300] * 9, 0, 0, F32),
+    # 16 rows a CTA: several row tiles
+    "r35_rows16_k": (7, 10, 2, [900, 2000], 500, 0.2, F32),
+    "r100_rows16": (25, 4, 1, [1000], 0, 0, BF16),
+    # 8 rows: one cluster, several of them, and slices through the workspace
+    "r4_clusters": (1, 4, 1, [30000, 9000], 0, 0, F32),
+    "r8_workspace_slices": (1, 64, 8, [6000, 100, 5000], 0, 0, BF16),
 }
 
 
@@ -550,59 +562,61 @@ def test_attention_of_many_rows(name, dev):
 
 
 @pytest.mark.parametrize("dt", [F32, BF16])
-@pytest.mark.parametrize("rising", [1, -1])
-def test_attention_of_many_rows_moves_its_reference(rising, dt, dev):
+@pytest.mark.parametrize("rising,L,Hkv", [(1, 8, 1), (-1, 8, 1), (1, 32, 6), (-1, 32, 6)])  # rows of 16, and of 128
+def test_attention_of_many_rows_moves_its_reference(rising, L, Hkv, dt, dev):
     """Logits that climb (or fall) by hundreds of units over a slice's tiles: sums and outputs move to new references,
     rows on their own; one row's logits stay."""
     rng = np.random.default_rng(7)
-    n, L, Hq = 1500, 8, 4
-    K, V = Cache([1536], 1, 128, dev), Cache([1536], 1, 128, dev)
-    k = rng.standard_normal((n, 1, 128))
-    k[:, 0, 0] = rising * np.linspace(-200, 200, n)
+    n, Hq = 1500, 4 * Hkv
+    K, V = Cache([1536], Hkv, 128, dev), Cache([1536], Hkv, 128, dev)
+    k = rng.standard_normal((n, Hkv, 128))
+    k[:, :, 0] = rising * np.linspace(-200, 200, n)[:, None]
     q8.append(K.codes[0], K.scales[0], k, n)
-    q8.append(V.codes[0], V.scales[0], rng.standard_normal((n, 1, 128)), n)
+    q8.append(V.codes[0], V.scales[0], rng.standard_normal((n, Hkv, 128)), n)
     K.upload(), V.upload()
     q = rng.standard_normal((L, 1, Hq, 128))
     q[:, 0, :, 0] = 12 * rng.random((L, Hq))
     q[0, 0, 0, 0] = 0
-    group_case(dev, rng, [n], L, Hq, 1, dt=dt, K=K, V=V, Qf=q)
-    group_case(dev, rng, [n], L, Hq, 1, k=900, dt=dt, K=K, V=V, Qf=q)
+    group_case(dev, rng, [n], L, Hq, Hkv, dt=dt, K=K, V=V, Qf=q)
+    group_case(dev, rng, [n], L, Hq, Hkv, k=900, dt=dt, K=K, V=V, Qf=q)
 
 
 @pytest.mark.parametrize("dt", [F32, BF16])
-def test_attention_of_many_rows_far_apart_scales(dt, dev):
+@pytest.mark.parametrize("L,Hkv", [(9, 1), (62, 16)])  # rows of 16, and of 128
+def test_attention_of_many_rows_far_apart_scales(L, Hkv, dt, dev):
     rng = np.random.default_rng(6)
     lens = [700, 130]
-    K, V = filled(rng, lens, 1, 128, dev, spread=1.0, strong=[(0, 3, 40), (0, 5, -40), (0, 7, 20), (1, 0, -60)])
-    group_case(dev, rng, lens, 9, 2, 1, dt=dt, K=K, V=V, scale=0.25)
-    group_case(dev, rng, lens, 9, 2, 1, k=250, dt=dt, K=K, V=V, scale=0.25)
+    K, V = filled(rng, lens, Hkv, 128, dev, spread=1.0, strong=[(0, 3, 40), (0, 5, -40), (0, 7, 20), (1, 0, -60)])
+    group_case(dev, rng, lens, L, 2 * Hkv, Hkv, dt=dt, K=K, V=V, scale=0.25)
+    group_case(dev, rng, lens, L, 2 * Hkv, Hkv, k=250, dt=dt, K=K, V=V, scale=0.25)
 
 
-def test_attention_of_many_rows_ignores_what_it_does_not_read(dev):
+@pytest.mark.parametrize("Hkv", [1, 80])  # rows of 16, and of 128
+def test_attention_of_many_rows_ignores_what_it_does_not_read(Hkv, dev):
     """NaN codes and scales past the length and in tokens the index does not name; a bad sequence; an entry past the
     length."""
     rng = np.random.default_rng(14)
     lens = [70, 300]
-    K, V = filled(rng, lens, 1, 128, dev)
+    K, V = filled(rng, lens, Hkv, 128, dev)
     for C in (K, V):
         for b, n in enumerate(lens):
             C.codes[b][:, n:] = 127
         C.codes[1][:, 5] = 127
         C.upload()
-    Qt = torch.from_numpy(rng.standard_normal((6, 2, 4, 128)).astype(np.float32)).to(BF16)
+    Qt = torch.from_numpy(rng.standard_normal((6, 2, 4 * Hkv, 128)).astype(np.float32)).to(BF16)
     idx = picks(rng, lens, 60)
     idx[1][idx[1] == 5] = -1
     args = (Qt.to(dev), *K.pair(), *V.pair(), i64(K.off, dev))
-    O = sa.decode_attn_q8(*args, i32(lens, dev), 300, 1, 0.1, idx=i32(idx, dev), out_dtype=F32)
-    check_attn(Qt.float().numpy(), K, V, lens, idx, 1, np.float32(0.1), O, F32)
+    O = sa.decode_attn_q8(*args, i32(lens, dev), 300, Hkv, 0.1, idx=i32(idx, dev), out_dtype=F32)
+    check_attn(Qt.float().numpy(), K, V, lens, idx, Hkv, np.float32(0.1), O, F32)
     idx[0, 7] = 70
     ws = sa.workspace(1 << 16, dev)
-    O = sa.decode_attn_q8(*args, i32(lens, dev), 300, 1, 0.1, idx=i32(idx, dev), out_dtype=F32, ws=ws)
+    O = sa.decode_attn_q8(*args, i32(lens, dev), 300, Hkv, 0.1, idx=i32(idx, dev), out_dtype=F32, ws=ws)
     code, det = status(ws)
     assert code == sa.SA_ERR_DEVICE and det == [12, 7, 70, 70]
-    check_attn(Qt.float().numpy(), K, V, lens, idx, 1, np.float32(0.1), O, F32)
+    check_attn(Qt.float().numpy(), K, V, lens, idx, Hkv, np.float32(0.1), O, F32)
     sa.clear_status(ws)
-    O = sa.decode_attn_q8(*args, i32([129, 300], dev), 300, 1, 0.1, idx=i32(idx, dev), out_dtype=F32, ws=ws)
+    O = sa.decode_attn_q8(*args, i32([129, 300], dev), 300, Hkv, 0.1, idx=i32(idx, dev), out_dtype=F32, ws=ws)
     code, det = status(ws)
     assert code == sa.SA_ERR_DEVICE and det[0] == 12 and det[1] == 0
     assert (O[:, 0] == 0).all() and not (O[:, 1] == 0).any()
