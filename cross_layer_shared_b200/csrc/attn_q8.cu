@@ -11,10 +11,10 @@
 // pass here).
 //
 //   * One CTA of 8 warps per (sequence, KV head, 8 or 16 query rows, slice of
-//     the keys), two CTAs per SM (much work of many rows: attn_q8_group.cu).  Each warp walks
-//     keys of its own 16 at a time with a ring of three stages (K and V codes
-//     and scales by cp.async, two passes ahead): warps never wait for one
-//     another.
+//     the keys), two CTAs per SM (much work of many rows: attn_q8_group.cu).
+//     Each warp walks keys of its own 16 at a time with a ring of three stages
+//     (K and V codes and scales by cp.async, two passes ahead): warps never
+//     wait for one another.
 //   * e4m3 codes become halves exactly (one conversion per two codes), in
 //     registers: S^T = K Q^T and O^T = V^T P^T are m16n8k16 f16 MMAs with fp32
 //     accumulators.  Queries are scaled per row by a power of two into the
@@ -33,7 +33,9 @@
 //     relative to the largest contribution, however far the scales are apart.
 //   * m_o moves only when some key passes it by more than 15 (log2 units) and
 //     is then set 7 below the maximum: weights stay below 2^15 and most of
-//     f16's range is above its subnormals.  l is a float: m_l moves past 60.
+//     f16's range is above its subnormals (a weight times its V scale keeps its
+//     bits down to 2^-21 of the row's largest, and one of 2^-32 is lost).  l is
+//     a float: m_l moves past 60.
 //   * Padding entries and tokens past the length have codes zero and weight
 //     zero, whatever the cache holds there.
 //   * Partial results travel normalised: (m, l, o / l).  A weighted mean of V
@@ -43,6 +45,11 @@
 //     much work each slice's) in the workspace and count themselves on a
 //     counter in its header; the last one merges them and puts the counter back
 //     to zero.  Results do not depend on which is last.
+//
+// Measured (B200, warm graph replay): every token of 4 x 131072, 32 query and 8
+// KV heads, 178 us = 92 % of the measured HBM rate; 8 sequences over 2048
+// picked tokens, 32 / 4 heads, 10.3 us (17 MB: latency); two sequences of 333
+// and 1021 tokens 6.4 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -13,11 +13,16 @@
 // piece of memory, and heads read far apart in time cost DRAM pages.
 //
 // A CTA's block is (blockIdx.y's sequence, block blockIdx.x / units behind its
-// first new token) where the sequences' counts are alike.  Ragged counts would leave
-// many such CTAs without work, each a place on the GPU for the time of a load
-// (16 prompts of 517 .. 16384 tokens: half of them, 30 of 165 us); there the
-// touched blocks are numbered through, and each warp finds its CTA's block by
-// a scan over the sequences, 32 at a time.
+// first new token) where the sequences' counts are alike.  Ragged counts would
+// leave many such CTAs without work, each a place on the GPU for the time of a
+// load (16 prompts of 517 .. 16384 tokens: half of them, 20 of 165 us); there
+// the touched blocks are numbered through, and each warp finds its CTA's block
+// by a scan over the sequences, 32 at a time.
+//
+// Measured (B200, warm graph replay): those 16 prompts, fp32, 4 heads of 128, K
+// and V, 122 us = 86 % of the measured HBM rate; 2048 bf16 tokens of 8 heads
+// 6.2 us; one token of 4 sequences 2.4 us.  Reading 131009 tokens of 8 heads
+// back as bf16 takes 121.7 us = the measured HBM rate.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>

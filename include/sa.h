@@ -594,8 +594,9 @@ sa_status sa_combine_partials(const float* O_part, int64_t o_stride, const float
  * the block's finite elements (2^-126 for a block of zeros); the code is the
  * e4m3 value nearest to x / scale, ties to the even code.  An element
  * carries a relative error of at most 2^-4, or 2^-17.8 of the block's
- * largest element where that is more.  (Readers take any finite scale >= 0;
- * one below 2^-126 counts as zero in sa_decode_attn_q8's values.)
+ * largest element where that is more.  (Readers also take other finite
+ * scales >= 0, of a cache from elsewhere: zero is a block of zeros; scale *
+ * code is then rounded where it is used, to bf16 at worst.)
  *
  *   K8, V8    e4m3 codes, n_tokens * Hkv rows of d: sequence b owns the token
  *             places [seq_off[b], seq_off[b+1]) (its capacity, cap_b of
@@ -671,12 +672,15 @@ sa_status sa_index_score_q8(const void* qI, const float* w, const void* KI8, con
  *   z_t = scale * Q[l,b,h,:] . K_b[g,t,:],   O[l,b,h,:] = sum_t softmax(z)_t * V_b[g,t,:]
  * over the tokens of idx[b,:] (entries < 0 skipped, a token listed twice
  * counts twice), or with idx = NULL and k = 0 over every token t <
- * seq_len[b] (a dense layer).  fp32 softmax and accumulation.  A row with no
- * token gets O = 0.  S_max >= every seq_len.  Supported: d = 128, Hq % Hkv ==
+ * seq_len[b] (a dense layer).  Softmax sums and accumulation are fp32; the
+ * weights enter the second product with 22 bits or more for fp32 outputs, 8
+ * or more (and divided by the sum of the rounded ones, or 11) for bf16
+ * outputs.  A row with no token gets O = 0.  S_max >= every seq_len.  Supported: d = 128, Hq % Hkv ==
  * 0, Hq/Hkv <= 128.
  * Device errors: idx entry >= seq_len[b] -> SA_ERR_DEVICE, entry skipped.
- * Keys are split over several CTAs whose partial results meet in the
- * workspace (counted in its header), whose size this gives: */
+ * Keys are split over several CTAs.  Where those are more than a cluster,
+ * their partial results meet in the workspace (some counted in its header),
+ * whose size this gives: */
 size_t sa_decode_attn_q8_workspace_size(int L_g, int B, int64_t n_tokens, int S_max, int Hq, int Hkv, int d, int k);
 sa_status sa_decode_attn_q8(const void* Q, const void* K8, const float* K_scale, const void* V8,
                             const float* V_scale, const int64_t* seq_off, const int32_t* seq_len,
