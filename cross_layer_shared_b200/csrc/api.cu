@@ -1317,7 +1317,7 @@ sa_status sa_cache_append_q8(const void* new_K, int64_t stride_K, const void* ne
   a.n_tokens = n_tokens;
   a.in_f32 = in_dtype == SA_F32;
   a.status = status_of(ws);
-  const cudaError_t e = sa::launch_cache_append_q8(a, (cudaStream_t)stream);
+  const cudaError_t e = sa::launch_cache_append_q8(a, num_sms(), (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail("sa_cache_append_q8 launch", e);
   return SA_OK;
 }

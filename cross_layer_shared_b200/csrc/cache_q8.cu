@@ -51,6 +51,11 @@ struct Raw8<false> {
     const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
     return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
   }
+  // largest |element| as bits, infinities and NaN included: pairs compared as integers
+  __device__ __forceinline__ uint32_t largest() const {
+    uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+    return max(m << 16, m & 0xffff0000u);
+  }
 };
 template <>
 struct Raw8<true> {
@@ -63,6 +68,12 @@ struct Raw8<true> {
   __device__ __forceinline__ float get(int i) const {
     const float4& q = i < 4 ? a : b;
     return (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w;
+  }
+  __device__ __forceinline__ uint32_t largest() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(get(i)) & 0x7fffffffu);
+    return m;
   }
 };
 
@@ -86,19 +97,33 @@ __device__ __forceinline__ NewTokens new_tokens(const Q8AppendArgs& a, int b, bo
   return t;
 }
 
-template <bool F32, int D, bool FLAT>
-__global__ void __launch_bounds__(kThreadsC) cache_append_q8_kernel(const Q8AppendArgs a) {
+// (tensor, head) units a CTA takes at once, with much to do: as many as make
+// 128 bytes a thread in flight
+template <bool F32, int D>
+constexpr int kUnits = 128 / (kQ8Block * D / kThreadsC * (F32 ? 4 : 2)) > 1
+                           ? 128 / (kQ8Block * D / kThreadsC * (F32 ? 4 : 2))
+                           : 1;
+
+// registers for as many CTAs an SM as hold what the memory needs in flight
+template <bool F32, int D, int U>
+constexpr int kAppendCtas = kQ8Block * D / kThreadsC * (F32 ? 4 : 2) * U < 128   ? 1
+                            : kQ8Block * D / kThreadsC * (F32 ? 4 : 2) * U == 128 ? 4
+                            : D == 192                                            ? 3
+                                                                                  : 2;
+
+template <bool F32, int D, bool FLAT, int U>
+__global__ void __launch_bounds__(kThreadsC, kAppendCtas<F32, D, U>) cache_append_q8_kernel(const Q8AppendArgs a) {
   constexpr int kPieces = D / 8;                           // 8-element pieces of a row
   constexpr int kPer = kQ8Block * kPieces / kThreadsC;     // pieces a thread holds
-  __shared__ uint32_t warp_max[kThreadsC / 32];
+  __shared__ uint32_t warp_max[U][kThreadsC / 32];
   const int tid = threadIdx.x;
   const int units = a.Hkv * (a.cache.codes[1] ? 2 : 1);  // (tensor, head)
-  const int unit = blockIdx.x % units;
-  const int h = unit % a.Hkv, which = unit / a.Hkv;
+  const int groups = (units + U - 1) / U;
+  const int unit0 = blockIdx.x % groups * U;
   pdl_trigger();
   pdl_wait();
   NewTokens nt;
-  int blk = blockIdx.x / units;  // block behind the sequence's first touched one
+  int blk = blockIdx.x / groups;  // block behind the sequence's first touched one
   if (FLAT) {
     const int lane = tid & 31;
     // one CTA more than there can be blocks: it meets every sequence
@@ -141,67 +166,85 @@ __global__ void __launch_bounds__(kThreadsC) cache_append_q8_kernel(const Q8Appe
   const int pos0 = s.len - nt.n;
   const int t0 = (nt.first + blk) * kQ8Block;  // the block's first token
   const int lo = max(pos0 - t0, 0), hi = min(s.len - t0, kQ8Block);  // new tokens [lo, hi) of the block
-  const int64_t row0 = s.off * a.Hkv + (int64_t)h * s.cap + t0;
-  float* scale_p = a.cache.scales[which] + row0 / kQ8Block;
-  uint32_t old_bits = 0;  // of the scale of the tokens already there (0: none, or not a positive scale)
-  if (lo > 0) {
-    const float old = __ldcg(scale_p);
-    if (old > 0.f && old < INFINITY) old_bits = __float_as_uint(old);
-  }
-  const uint8_t* src = reinterpret_cast<const uint8_t*>(a.rows[which]);
   constexpr int kElem = F32 ? 4 : 2;
-  const int64_t stride = a.stride[which];
-  Raw8<F32> x[kPer];
+  Raw8<F32> x[U][kPer];
+  uint32_t old_bits[U];  // of the scale of the tokens already there (0: none, or not a positive scale)
+  auto first_row = [&](int h) { return s.off * a.Hkv + (int64_t)h * s.cap + t0; };
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int r = (tid + i * kThreadsC) / kPieces, p = (tid + i * kThreadsC) % kPieces;
-    if (r >= lo && r < hi)
-      x[i].load(src + ((src0 + (t0 + r - pos0)) * stride + (int64_t)h * D + p * 8) * kElem);
-    else
-      x[i].clear();
+  for (int u = 0; u < U; ++u) {
+    const int unit = unit0 + u, which = unit >= a.Hkv, h = unit - which * a.Hkv;
+    old_bits[u] = 0;
+    if (lo > 0 && unit < units) {
+      const float old = __ldcg(a.cache.scales[which] + first_row(h) / kQ8Block);
+      if (old > 0.f && old < INFINITY) old_bits[u] = __float_as_uint(old);
+    }
+    const uint8_t* src = reinterpret_cast<const uint8_t*>(a.rows[which]);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int r = (tid + i * kThreadsC) / kPieces, p = (tid + i * kThreadsC) % kPieces;
+      if (r >= lo && r < hi && unit < units)
+        x[u][i].load(src + ((src0 + (t0 + r - pos0)) * a.stride[which] + (int64_t)h * D + p * 8) * kElem);
+      else
+        x[u][i].clear();
+    }
   }
   // max|x| over the finite values, as bits (ordered like the floats)
-  uint32_t mx = 0;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i)
+  for (int u = 0; u < U; ++u) {
+    uint32_t mx = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t u = __float_as_uint(x[i].get(j)) & 0x7fffffffu;
-      mx = max(mx, u < 0x7f800000u ? u : 0u);
+    for (int i = 0; i < kPer; ++i) mx = max(mx, x[u][i].largest());
+    if (mx >= 0x7f800000u) {  // an infinity or NaN among them
+      mx = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t v = __float_as_uint(x[u][i].get(j)) & 0x7fffffffu;
+          mx = max(mx, v < 0x7f800000u ? v : 0u);
+        }
     }
-  mx = __reduce_max_sync(0xffffffffu, mx);
-  if ((tid & 31) == 0) warp_max[tid >> 5] = mx;
+    mx = __reduce_max_sync(0xffffffffu, mx);
+    if ((tid & 31) == 0) warp_max[u][tid >> 5] = mx;
+  }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kThreadsC / 32; ++i) mx = max(mx, warp_max[i]);
-  const uint32_t bits = max(q8_scale_bits(mx), old_bits);
-  const float inv = 1.f / __uint_as_float(bits);  // exact: a power of two
-  uint8_t* dst = a.cache.codes[which] + row0 * D;
-  const bool move = lo > 0 && bits != old_bits;  // the tokens already there go to the larger scale
-  const float ratio = move ? __uint_as_float(old_bits) * inv : 1.f;
+  for (int u = 0; u < U; ++u) {
+    const int unit = unit0 + u, which = unit >= a.Hkv, h = unit - which * a.Hkv;
+    if (unit >= units) return;
+    uint32_t mx = 0;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int r = (tid + i * kThreadsC) / kPieces, p = (tid + i * kThreadsC) % kPieces;
-    uint2* out = reinterpret_cast<uint2*>(dst + r * D + p * 8);
-    if (r >= lo && r < hi) {
-      *out = make_uint2(
-          q8_from_float4(x[i].get(0) * inv, x[i].get(1) * inv, x[i].get(2) * inv, x[i].get(3) * inv),
-          q8_from_float4(x[i].get(4) * inv, x[i].get(5) * inv, x[i].get(6) * inv, x[i].get(7) * inv));
-    } else if (r < lo && move) {
-      const uint2 c = *out;
-      uint32_t q[2] = {c.x, c.y};
+    for (int i = 0; i < kThreadsC / 32; ++i) mx = max(mx, warp_max[u][i]);
+    const uint32_t bits = max(q8_scale_bits(mx), old_bits[u]);
+    const float inv = 1.f / __uint_as_float(bits);  // exact: a power of two
+    const int64_t row0 = first_row(h);
+    uint8_t* dst = a.cache.codes[which] + row0 * D;
+    const bool move = lo > 0 && bits != old_bits[u];  // the tokens already there go to the larger scale
+    const float ratio = move ? __uint_as_float(old_bits[u]) * inv : 1.f;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        uint32_t l, u;
-        q8_to_half4(q[j], l, u);
-        const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&l));
-        const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&u));
-        q[j] = q8_from_float4(f0.x * ratio, f0.y * ratio, f1.x * ratio, f1.y * ratio);
+    for (int i = 0; i < kPer; ++i) {
+      const int r = (tid + i * kThreadsC) / kPieces, p = (tid + i * kThreadsC) % kPieces;
+      uint2* out = reinterpret_cast<uint2*>(dst + r * D + p * 8);
+      if (r >= lo && r < hi) {
+        const Raw8<F32>& v = x[u][i];
+        *out = make_uint2(q8_from_float4(v.get(0) * inv, v.get(1) * inv, v.get(2) * inv, v.get(3) * inv),
+                          q8_from_float4(v.get(4) * inv, v.get(5) * inv, v.get(6) * inv, v.get(7) * inv));
+      } else if (r < lo && move) {
+        const uint2 c = *out;
+        uint32_t q[2] = {c.x, c.y};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          uint32_t l, u2;
+          q8_to_half4(q[j], l, u2);
+          const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&l));
+          const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&u2));
+          q[j] = q8_from_float4(f0.x * ratio, f0.y * ratio, f1.x * ratio, f1.y * ratio);
+        }
+        *out = make_uint2(q[0], q[1]);
       }
-      *out = make_uint2(q[0], q[1]);
     }
+    if (tid == 0 && bits != old_bits[u]) a.cache.scales[which][row0 / kQ8Block] = __uint_as_float(bits);
   }
-  if (tid == 0 && bits != old_bits) *scale_p = __uint_as_float(bits);
 }
 
 // ---------------------------------------------------------------- reading back
@@ -328,24 +371,33 @@ cudaError_t launch_grid(Kernel kern, const Args& a, dim3 grid, cudaStream_t stre
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-}  // namespace
-
-cudaError_t launch_cache_append_q8(const Q8AppendArgs& a, cudaStream_t stream) {
+template <bool F32, int D>
+cudaError_t launch_append(const Q8AppendArgs& a, int num_sms, cudaStream_t stream) {
   // blocks a sequence's new tokens can touch: one more than full blocks when they start inside one
   const int64_t blocks = ((int64_t)a.max_new + kQ8Block - 2) / kQ8Block + 1;
   // and all of them together: less than two more than full blocks each
   const int64_t all = a.n_rows / kQ8Block + 2ll * a.B + 1;
   const int units = a.Hkv * (a.cache.codes[1] ? 2 : 1);
   const bool flat = blocks * a.B > all + all / 4;
-  const dim3 grid((unsigned)((flat ? all : blocks) * units), flat ? 1 : a.B);
-#define SA_APPEND_CASE(DD)                                                                      \
-  if (a.d == DD) {                                                                              \
-    if (flat)                                                                                   \
-      return a.in_f32 ? launch_grid(cache_append_q8_kernel<true, DD, true>, a, grid, stream)    \
-                      : launch_grid(cache_append_q8_kernel<false, DD, true>, a, grid, stream);  \
-    return a.in_f32 ? launch_grid(cache_append_q8_kernel<true, DD, false>, a, grid, stream)     \
-                    : launch_grid(cache_append_q8_kernel<false, DD, false>, a, grid, stream);   \
-  }
+  constexpr int U = kUnits<F32, D>;
+  // several units a CTA from two waves on: a CTA's fixed second half of its
+  // time (place, reduction, launch) then moves more bytes (22 sequences of
+  // 1107 .. 2215 bf16 tokens, 4 heads of 128: 32 us, 37 with one)
+  const bool many = U > 1 && units > 1 && (flat ? all : blocks * a.B) * units > 12ll * num_sms;
+  const int groups = many ? (units + U - 1) / U : units;
+  const dim3 grid((unsigned)((flat ? all : blocks) * groups), flat ? 1 : a.B);
+  if (many)
+    return flat ? launch_grid(cache_append_q8_kernel<F32, D, true, U>, a, grid, stream)
+                : launch_grid(cache_append_q8_kernel<F32, D, false, U>, a, grid, stream);
+  return flat ? launch_grid(cache_append_q8_kernel<F32, D, true, 1>, a, grid, stream)
+              : launch_grid(cache_append_q8_kernel<F32, D, false, 1>, a, grid, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_append_q8(const Q8AppendArgs& a, int num_sms, cudaStream_t stream) {
+#define SA_APPEND_CASE(DD) \
+  if (a.d == DD) return a.in_f32 ? launch_append<true, DD>(a, num_sms, stream) : launch_append<false, DD>(a, num_sms, stream);
   SA_APPEND_CASE(64) SA_APPEND_CASE(128) SA_APPEND_CASE(192) SA_APPEND_CASE(256)
 #undef SA_APPEND_CASE
   return cudaErrorInvalidValue;

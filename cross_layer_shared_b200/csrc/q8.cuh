@@ -116,7 +116,7 @@ struct Q8AppendArgs {
   int in_f32;
   DeviceStatus* status;
 };
-cudaError_t launch_cache_append_q8(const Q8AppendArgs& a, cudaStream_t stream);
+cudaError_t launch_cache_append_q8(const Q8AppendArgs& a, int num_sms, cudaStream_t stream);
 
 struct Q8ReadArgs {
   Q8Cache cache;

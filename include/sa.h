@@ -661,7 +661,8 @@ sa_status sa_cache_read_q8(const void* K8, const float* K_scale, const void* V8,
  * seq_len[b] are left untouched.  The queries stay bf16 (finite): they enter
  * the products as two e4m3 parts, exact but for elements below 2^-11 of their
  * row's largest, which are off by at most 2^-17 of it.
- * Supported: 1 <= H_I <= 64, d_I in {64, 128, 192, 256}. */
+ * A product that is NaN (a NaN code) counts as 0, as in
+ * sa_index_score.  Supported: 1 <= H_I <= 64, d_I in {64, 128, 192, 256}. */
 sa_status sa_index_score_q8(const void* qI, const float* w, const void* KI8, const float* KI_scale,
                             const int64_t* seq_off, const int32_t* seq_len, int B, int64_t n_tokens, int S_max,
                             int H_I, int d_I, float* scores, int64_t ld, void* ws, size_t ws_bytes, void* stream);
