@@ -265,10 +265,12 @@ __global__ void __launch_bounds__(kThreadsQ, 2) attn_q8_kernel(const Q8AttnArgs 
   for (int p = 0; p < n_pass; ++p) {
     cp_async_wait<1>();
     __syncwarp();  // pass p has landed; pass p - 1's stage is free
-    const bool seen0 = seen >> gq & 1, seen1 = seen >> (gq + 8) & 1;
+    const uint32_t here = seen;
+    const bool seen0 = here >> gq & 1, seen1 = here >> (gq + 8) & 1;
     seen = seen_after;
     seen_after = issue(t_next, p + 2);
     t_next = entry(p + 3);
+    if (here == 0u) continue;  // padding: the end of a short sequence's index
     const StageQ& st = sm.ring[warp][p % kStagesQ];
     // ---- S^T = K Q^T: lane holds keys gq, gq + 8 at rows 2tq, 2tq + 1 ----
     float sc[NT][2][4];

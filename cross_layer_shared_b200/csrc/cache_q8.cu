@@ -106,8 +106,8 @@ constexpr int kUnits = 128 / (kQ8Block * D / kThreadsC * (F32 ? 4 : 2)) > 1
 
 // registers for as many CTAs an SM as hold what the memory needs in flight
 template <bool F32, int D, int U>
-constexpr int kAppendCtas = kQ8Block * D / kThreadsC * (F32 ? 4 : 2) * U < 128   ? 1
-                            : kQ8Block * D / kThreadsC * (F32 ? 4 : 2) * U == 128 ? 4
+constexpr int kAppendCtas = kQ8Block * D / kThreadsC * (F32 ? 4 : 2) * U < 96    ? 1
+                            : kQ8Block * D / kThreadsC * (F32 ? 4 : 2) * U <= 128 ? 4
                             : D == 192                                            ? 3
                                                                                   : 2;
 
