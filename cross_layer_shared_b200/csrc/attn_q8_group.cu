@@ -131,6 +131,13 @@ __device__ __forceinline__ void tmem_set(uint32_t at, float v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(at), "r"(__float_as_uint(v)) : "memory");
 }
 
+// True in one lane of a converged warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // Both phases, by every lane: no broadcast, and most often no wait.
 __device__ __forceinline__ bool warp_wait_both(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb) {
   const bool ready = mbar_try_wait(a, pa) & mbar_try_wait(b, pb);
@@ -324,56 +331,65 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
   } else if (warp == kMmaWarp) {
     // =============== MMA issuer ===============
     ready();
-    const uint32_t tmem = *slot;
-    if (lane == 0 && nt > 0) {
+    // The whole warp stays together and one elected lane issues: operands of a
+    // product are then known to be one value per warp.
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *slot, 0);
+    const bool lead = elect_one();
+    auto wait = [](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitLimitNs));
+    };
+    if (nt > 0) {
       constexpr uint32_t idesc_qk = umma_idesc_bf16(128, 128, false, false);
       constexpr uint32_t idesc_l = umma_idesc_bf16(128, 16, false, false);
       constexpr uint32_t idesc_pv = umma_idesc_bf16(128, 128, false, true);
       auto pv = [&](int i) -> bool {
-        if (!mbar_wait(&v_full[i % SV], (i / SV) & 1, kWaitLimitNs) ||
-            !mbar_wait(&p_full[i & 1], (i >> 1) & 1, kWaitLimitNs))
-          return false;
+        if (!wait(&v_full[i % SV], (i / SV) & 1) || !wait(&p_full[i & 1], (i >> 1) & 1)) return false;
         tc_fence_after();
         const uint32_t pst = sbase + Lay::kK + i % SK * kTileG;  // P lives here now
         const uint32_t vst = sbase + Lay::kV + i % SV * kTileG;
+        if (lead) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {  // keys 64h + 16kk ..
-            const uint64_t vd = umma_desc_sw128(vst + h * 8192 + kk * 2048, kHalfG, 1024);
+            for (int kk = 0; kk < 4; ++kk) {  // keys 64h + 16kk ..
+              const uint64_t vd = umma_desc_sw128(vst + h * 8192 + kk * 2048, kHalfG, 1024);
 #pragma unroll
-            for (int q = 0; q < Lay::kParts; ++q) {
-              const uint64_t pd = umma_desc_sw128(
-                  (q == 0 ? pst : sbase + Lay::kPlo + (q - 1) * kTileG) + h * kHalfG + kk * 32, 16, 1024);
-              umma_bf16(tmem + 256, pd, vd, idesc_pv, (i | h | kk | q) != 0);
-              umma_bf16(tmem + 384, pd, umma_desc_sw128(sbase + Lay::kOnes + h * 2048 + kk * 32, 16, 1024), idesc_l,
-                        (i | h | kk | q) != 0);
+              for (int q = 0; q < Lay::kParts; ++q) {
+                const uint64_t pd = umma_desc_sw128(
+                    (q == 0 ? pst : sbase + Lay::kPlo + (q - 1) * kTileG) + h * kHalfG + kk * 32, 16, 1024);
+                umma_bf16(tmem + 256, pd, vd, idesc_pv, (i | h | kk | q) != 0);
+                umma_bf16(tmem + 384, pd, umma_desc_sw128(sbase + Lay::kOnes + h * 2048 + kk * 32, 16, 1024), idesc_l,
+                          (i | h | kk | q) != 0);
+              }
             }
-          }
-        umma_commit(&k_empty[i % SK]);
-        umma_commit(&v_empty[i % SV]);
-        umma_commit(&o_done[i & 3]);
+          umma_commit(&k_empty[i % SK]);
+          umma_commit(&v_empty[i % SV]);
+          umma_commit(&o_done[i & 3]);
+        }
+        __syncwarp();
         return true;
       };
-      bool ok = mbar_wait(q_full, 0, kWaitLimitNs);
+      bool ok = wait(q_full, 0);
       for (int j = 0; j < nt && ok; ++j) {
         if (PRECISE && j >= 1 && !(ok = pv(j - 1))) break;  // the next K tile follows it
-        ok = mbar_wait(&k_full[j % SK], (j / SK) & 1, kWaitLimitNs) &&
-             mbar_wait(&s_free[j & 1], ((j >> 1) & 1) ^ 1, kWaitLimitNs);
+        ok = wait(&k_full[j % SK], (j / SK) & 1) && wait(&s_free[j & 1], ((j >> 1) & 1) ^ 1);
         if (!ok) break;
         tc_fence_after();
         const uint32_t kst = sbase + Lay::kK + j % SK * kTileG;
+        if (lead) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_bf16(tmem + (j & 1) * 128, umma_desc_sw128(sbase + h * kHalfG + kk * 32, 16, 1024),
-                      umma_desc_sw128(kst + h * kHalfG + kk * 32, 16, 1024), idesc_qk, (h | kk) != 0);
-        umma_commit(&s_full[j & 1]);
+            for (int kk = 0; kk < 4; ++kk)
+              umma_bf16(tmem + (j & 1) * 128, umma_desc_sw128(sbase + h * kHalfG + kk * 32, 16, 1024),
+                        umma_desc_sw128(kst + h * kHalfG + kk * 32, 16, 1024), idesc_qk, (h | kk) != 0);
+          umma_commit(&s_full[j & 1]);
+        }
+        __syncwarp();
         if (!PRECISE && j >= 1) ok = pv(j - 1);
       }
       if (ok) ok = pv(nt - 1);
-      if (!ok) report(a.status, kErrTimeout, kKernAttnQ8, blockIdx.x, 1, 0);
+      if (!ok && lane == 0) report(a.status, kErrTimeout, kKernAttnQ8, blockIdx.x, 1, 0);
     }
   } else {
     // =============== queries, then softmax ===============
