@@ -189,7 +189,9 @@ __global__ void __launch_bounds__(kThreadsG, 1) attn_q8_group_kernel(const Q8Att
   using Lay = SmemG<PRECISE>;
   constexpr int SK = Lay::kStagesK, SV = Lay::kStagesV;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (an offset, not a rounded address: the compiler then knows it for shared
+  // memory; generic loads would queue behind the global ones)
+  uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
   const uint32_t sbase = smem_u32(smem);
   uint32_t* seen_s = reinterpret_cast<uint32_t*>(smem + Lay::kSeen);
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + Lay::kBar);

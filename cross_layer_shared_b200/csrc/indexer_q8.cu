@@ -101,7 +101,9 @@ indexer_q8_kernel(const __grid_constant__ CUtensorMap tm_ki, const Q8IndexerArgs
   using Lay = LayoutI<NH, NPAD>;
   constexpr int kAcc = Lay::kAcc;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (an offset, not a rounded address: the compiler then knows it for shared
+  // memory; generic loads would queue behind the global ones)
+  uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem);
   uint64_t* empty = full + kMaxStagesI;
   uint64_t* tfull = empty + kMaxStagesI;
