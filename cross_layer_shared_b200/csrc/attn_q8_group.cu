@@ -131,13 +131,6 @@ __device__ __forceinline__ void tmem_set(uint32_t at, float v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(at), "r"(__float_as_uint(v)) : "memory");
 }
 
-// True in one lane of a converged warp, always the same one.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
-  return p != 0;
-}
-
 // Both phases, by every lane: no broadcast, and most often no wait.
 __device__ __forceinline__ bool warp_wait_both(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb) {
   const bool ready = mbar_try_wait(a, pa) & mbar_try_wait(b, pb);

@@ -155,7 +155,7 @@ indexer_q8_kernel(const __grid_constant__ CUtensorMap tm_ki, const Q8IndexerArgs
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t tmem_base = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   // this CTA's tiles [g_beg, g_end), and the sequence of the first
   const int total = prefix[a.B];
   const int g_beg = (int)((int64_t)total * blockIdx.x / gridDim.x);
@@ -194,33 +194,38 @@ indexer_q8_kernel(const __grid_constant__ CUtensorMap tm_ki, const Q8IndexerArgs
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_e4m3(128, Lay::kCols);
-      const uint64_t a0 = umma_desc_sw128(smem_u32(ring), 16, 1024);
-      const uint64_t b0 = umma_desc_sw128(smem_u32(qbuf), 16, 1024);
-      int st = 0, nseq = 0;
-      uint32_t phase = 0;
-      int next = g_beg;  // first tile of the next sequence
-      for (int g = g_beg, i = 0; g < g_end; ++g, ++i) {
-        const int c = i % kAcc;
-        bool ok = true;
-        if (g == next) {
-          while (g >= prefix[b + 1]) ++b;
-          next = prefix[b + 1];
-          if (nseq > 0) umma_commit(&qempty[(nseq - 1) & 1]);  // the last sequence's products
-          ok = mbar_wait(&qfull[nseq & 1], (nseq >> 1) & 1, kWaitLimitNs);
-          ++nseq;
-        }
-        if (!ok || !mbar_wait(&full[st], phase, kWaitLimitNs) ||
-            !mbar_wait(&tempty[c], ((i / kAcc) & 1) ^ 1, kWaitLimitNs)) {
-          report(a.status, kErrTimeout, kKernIndexerQ8, blockIdx.x, 1, i);
-          break;
-        }
-        tc_fence_after();
-        // descriptors count 16-byte units
-        const uint64_t ad = a0 + (uint32_t)(st * (Lay::kStageBytes / 16));
-        const uint64_t bd = b0 + ((nseq - 1) & 1) * (uint32_t)(Lay::kQBytes / 16);
-        const uint32_t d = tmem_base + c * Lay::kCols;
+    // the warp stays together and one elected lane issues: a product's operands
+    // are then known to be one value per warp
+    const bool lead = elect_one();
+    auto wait = [](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitLimitNs));
+    };
+    constexpr uint32_t idesc = idesc_e4m3(128, Lay::kCols);
+    const uint64_t a0 = umma_desc_sw128(smem_u32(ring), 16, 1024);
+    const uint64_t b0 = umma_desc_sw128(smem_u32(qbuf), 16, 1024);
+    int st = 0, nseq = 0;
+    uint32_t phase = 0;
+    int next = g_beg;  // first tile of the next sequence
+    for (int g = g_beg, i = 0; g < g_end; ++g, ++i) {
+      const int c = i % kAcc;
+      bool ok = true;
+      if (g == next) {
+        while (g >= prefix[b + 1]) ++b;
+        next = prefix[b + 1];
+        if (nseq > 0 && lead) umma_commit(&qempty[(nseq - 1) & 1]);  // the last sequence's products
+        ok = wait(&qfull[nseq & 1], (nseq >> 1) & 1);
+        ++nseq;
+      }
+      if (!ok || !wait(&full[st], phase) || !wait(&tempty[c], ((i / kAcc) & 1) ^ 1)) {
+        if (lane == 0) report(a.status, kErrTimeout, kKernIndexerQ8, blockIdx.x, 1, i);
+        break;
+      }
+      tc_fence_after();
+      // descriptors count 16-byte units
+      const uint64_t ad = a0 + (uint32_t)(st * (Lay::kStageBytes / 16));
+      const uint64_t bd = b0 + ((nseq - 1) & 1) * (uint32_t)(Lay::kQBytes / 16);
+      const uint32_t d = tmem_base + c * Lay::kCols;
+      if (lead) {
 #pragma unroll
         for (int k = 0; k < NH * 4; ++k) {
           if (k >= ksteps) break;
@@ -229,8 +234,9 @@ indexer_q8_kernel(const __grid_constant__ CUtensorMap tm_ki, const Q8IndexerArgs
         }
         umma_commit(&empty[st]);
         umma_commit(&tfull[c]);
-        if (++st == n_st) st = 0, phase ^= 1;
       }
+      __syncwarp();
+      if (++st == n_st) st = 0, phase ^= 1;
     }
   } else if (warp < 6) {
     // ---------------- epilogue: ReLU, head weights, sum, key scale ----------------

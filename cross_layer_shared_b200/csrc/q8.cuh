@@ -45,6 +45,13 @@ __device__ __forceinline__ Q8Seq q8_seq(const int64_t* seq_off, const int32_t* s
   return s;
 }
 
+// True in one lane of a converged warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // ---- conversions ----
 // four e4m3 codes -> four halves (exact), two per register
 __device__ __forceinline__ void q8_to_half4(uint32_t c, uint32_t& lo, uint32_t& hi) {
