@@ -32,10 +32,14 @@
 //     through the workspace and a second kernel, one row per warp.
 //
 // Measured (B200, warm graph replay): 24 layers of 32 query and 8 KV heads (96
-// rows) over 2048 picked tokens of 4 sequences 18.8 us, of which 4.3 go by
+// rows) over 2048 picked tokens of 4 sequences 18.2 us, of which 4.3 go by
 // before the first S, 7 over four tiles and 5 on the last products, the
-// cluster's barrier and the merge.  Many tiles take 2.1 us each: the softmax
-// warps, whose instructions are what a tile waits for.
+// cluster's barrier and the merge.  Many tiles take 2.1 us each, and the
+// producers set that pace: about 3200 cycles for a tile's loads and stores of K,
+// then V, and the memory behind them; the softmax needs 2100, the products 1500.
+// Four producer warps for K and four for V, without barriers among them, are
+// faster over many tiles (246 for 278 us, 20 rows over 65,536 tokens of 32
+// sequences and heads) and slower over the four of a picked step (18.8): not taken.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>

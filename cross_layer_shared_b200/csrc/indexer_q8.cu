@@ -24,8 +24,8 @@
 // sequences of 8192 .. 131072: 90, 54 and 61 us with 1, 2 and 3 CTAs an SM).
 //
 // Measured (B200, warm graph replay, 16 heads of 128): those 32 sequences 54 us
-// = 83 % of the measured HBM rate, 4 x 131072 keys 17.4 us; one sequence of 4096
-// keys, 4 heads of 64, 3.9 us.
+// = 84 % of the measured HBM rate, 4 x 131072 keys 17.0 us; one sequence of 4096
+// keys, 4 heads of 64, 3.5 us.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
