@@ -126,12 +126,14 @@ __device__ __forceinline__ void cp_async4(void* dst, const void* src, uint32_t s
                : "memory");
 }
 
-// a scale >= 0 as f 2^e, 1 <= f < 2; (0, 0) for one below 2^-126
+// a scale >= 0 as f 2^e, 1 <= f < 2.  Zero has f = 0 and an exponent below
+// every other one's, so that a key without a contribution does not set the
+// reference of those that have one.
 __device__ __forceinline__ void split_scale(float s, float& f, float& e) {
-  const uint32_t u = __float_as_uint(s);
-  const int x = (int)(u >> 23 & 0xff);
-  f = x == 0 ? 0.f : __uint_as_float((u & 0x7fffffu) | 0x3f800000u);
-  e = x == 0 ? 0.f : (float)(x - 127);
+  const bool tiny = s < 0x1p-126f;  // zero or subnormal: normalised first
+  const uint32_t u = __float_as_uint(tiny ? s * 0x1p24f : s);
+  f = s == 0.f ? 0.f : __uint_as_float((u & 0x7fffffu) | 0x3f800000u);
+  e = (float)((int)(u >> 23 & 0xff) - (tiny ? 127 + 24 : 127));
 }
 
 // max over the 8 lanes that hold one query row's keys
