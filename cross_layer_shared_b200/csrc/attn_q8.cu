@@ -31,11 +31,11 @@
 //     joins the logit: o sums f 2^(z + e - m_o) cv with a reference m_o over
 //     z + e of its own, l sums 2^(z - m_l).  So a key's weight is held
 //     relative to the largest contribution, however far the scales are apart.
-//   * m_o moves only when some key passes it by more than 15 (log2 units) and
-//     is then set 7 below the maximum: weights stay below 2^15 and most of
-//     f16's range is above its subnormals (a weight times its V scale keeps its
-//     bits down to 2^-21 of the row's largest, and one of 2^-32 is lost).  l is
-//     a float: m_l moves past 60.
+//   * m_o moves only when some key passes it by more than 14 (log2 units) and
+//     is then set 7 below the maximum: weights, f < 2 included, stay below
+//     2^15 and most of f16's range is above its subnormals (a weight times its
+//     V scale keeps its bits down to 2^-21 of the row's largest, and one of
+//     2^-32 is lost).  l is a float: m_l moves past 60.
 //   * Padding entries and tokens past the length have codes zero and weight
 //     zero, whatever the cache holds there.
 //   * Partial results travel normalised: (m, l, o / l).  A weighted mean of V
@@ -70,6 +70,7 @@ constexpr int kWarpsQ = 8;
 constexpr int kThreadsQ = kWarpsQ * 32;
 constexpr int kKeysQ = 16;   // keys of a pass
 constexpr int kStagesQ = 3;
+constexpr float kRangeO = 14.f;  // log2 units z + e may pass m_o by: 2^14 f is finite in f16 for any f < 2
 constexpr int kORow = kDq + 4;
 
 struct StageQ {
@@ -315,7 +316,7 @@ __global__ void __launch_bounds__(kThreadsQ, 2) attn_q8_kernel(const Q8AttnArgs 
       for (int e = 0; e < 2; ++e) {
         z[n][e] = seen0 ? (sc[n][0][e] + sc[n][1][e]) * (ks0 * rf[n][e]) : -INFINITY;
         z[n][2 + e] = seen1 ? (sc[n][0][2 + e] + sc[n][1][2 + e]) * (ks1 * rf[n][e]) : -INFINITY;
-        over |= fmaxf(z[n][e] + e0, z[n][2 + e] + e1) > m_o[n][e] + 15.f;
+        over |= fmaxf(z[n][e] + e0, z[n][2 + e] + e1) > m_o[n][e] + kRangeO;
         over |= fmaxf(z[n][e], z[n][2 + e]) > m_l[n][e] + 60.f;
       }
     if (__any_sync(0xffffffffu, over)) {
@@ -330,7 +331,7 @@ __global__ void __launch_bounds__(kThreadsQ, 2) attn_q8_kernel(const Q8AttnArgs 
             l_run[n][e] *= m_l[n][e] == -INFINITY ? 0.f : ex2f(m_l[n][e] - ml);
             m_l[n][e] = ml;
           }
-          if (mo > m_o[n][e] + 15.f) {
+          if (mo > m_o[n][e] + kRangeO) {
             alpha[e] = m_o[n][e] == -INFINITY ? 0.f : ex2f(m_o[n][e] - (mo - 7.f));
             m_o[n][e] = mo - 7.f;
           }

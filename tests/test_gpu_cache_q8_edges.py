@@ -53,3 +53,17 @@ def test_scales_below_the_smallest_normal_number(dev):
     idx = np.arange(48)[None] % 3 * 64 + np.arange(48)[None] // 3
     O = attend(dev, K, V, [192], rng.standard_normal((1, 1, 4, 128)), 2, idx)
     assert O.abs().max().item() > 1e-37
+
+
+@pytest.mark.parametrize("dt", [F32, BF16])
+@pytest.mark.parametrize("k", [0, 192])
+@pytest.mark.parametrize("high", [511.99, 255.999, 448.0, 2.0 ** 9 * (1 - 2.0 ** -24)])
+def test_a_scale_just_under_a_power_of_two(high, k, dt, dev):
+    """A later block's V scale passes the first one's by as much as the reference allows, times almost two: the
+    weights that meet in the second product stay finite."""
+    rng = np.random.default_rng(62)
+    K, V = filled(rng, [192], 1, 128, dev)
+    V.scales[0][:] = np.array([1.0, 1.0, np.float32(high)])
+    V.upload()
+    idx = np.arange(192)[None] if k else None
+    attend(dev, K, V, [192], np.zeros((1, 1, 4, 128)), 1, idx, dt)
