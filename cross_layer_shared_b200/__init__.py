@@ -913,8 +913,9 @@ def decode_step_q8(pattern: str, qI: Sequence, w: Sequence, KI: Sequence, K: Seq
     sequences.  An F layer scores its keys and picks the top-k tokens; it and
     the S layers behind it attend to them, neighbours that share a cache in
     one launch.  With new_KI ([B, 1, d_I]), new_K and new_V ([B, Hkv, d]) per
-    layer, the new token's rows are quantised into the caches first, into a
-    cache that several layers list once, from the first of them.  Returns
+    layer, the new token's rows are quantised into the caches first, into each
+    cache once: from the first layer that lists it (and, where a layer's K and
+    V are one cache, from new_K).  Returns
     (O, idx of the last F layer)."""
     L, B, Hq, d = Q.shape
     n = len(pattern)
@@ -947,8 +948,13 @@ def decode_step_q8(pattern: str, qI: Sequence, w: Sequence, KI: Sequence, K: Seq
                 cache_append_q8(new_KI[l], None, *KI[l], None, None, seq_off, seq_len, ws=ws, stream=stream)
     if new_K is not None:
         for l in range(n):
-            if first(K[l]):
+            # layers may share one of K and V, and K and V may be one cache
+            todo = [(x, c) for x, c in ((new_K[l], K[l]), (new_V[l], V[l])) if first(c)]
+            if len(todo) == 2:
                 cache_append_q8(new_K[l], new_V[l], *K[l], *V[l], seq_off, seq_len, ws=ws, stream=stream)
+            else:
+                for x, c in todo:
+                    cache_append_q8(x, None, *c, None, None, seq_off, seq_len, ws=ws, stream=stream)
     l = 0
     while l < n:
         if pattern[l] == "F":

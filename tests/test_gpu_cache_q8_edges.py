@@ -67,3 +67,42 @@ def test_a_scale_just_under_a_power_of_two(high, k, dt, dev):
     V.upload()
     idx = np.arange(192)[None] if k else None
     attend(dev, K, V, [192], np.zeros((1, 1, 4, 128)), 1, idx, dt)
+
+
+# ------------------------------------------------------------------ a step whose layers share half of a cache
+@pytest.mark.parametrize("layers", [[("KA", "VA"), ("KA", "VB"), ("KB", "VB")], [("KA", "KA"), ("KA", "VA"), ("VA", "KA")]],
+                         ids=["half_shared", "one_cache_as_both"])
+def test_step_appends_to_every_listed_cache_once(layers, dev):
+    """Layers that share K and not V, V and not K, and layers whose K and V are one cache: each cache gets one row
+    per sequence, from the first place that lists it (a layer's K before its V)."""
+    rng = np.random.default_rng(63)
+    lens, Hkv = [70, 127], 2
+    new_lens = [n + 1 for n in lens]
+    C = {}
+    for name in sorted({name for pair in layers for name in pair}):
+        C[name], _ = filled(rng, lens, Hkv, 128, dev)
+    KI, _ = filled(rng, lens, 1, 64, dev)
+    for c in list(C.values()) + [KI]:  # room for one token more in every sequence
+        assert all(n <= cap for n, cap in zip(new_lens, c.caps))
+    L = len(layers)
+    new_K, new_V = ([rows(rng, 2, Hkv, 128, BF16) for _ in range(L)] for _ in range(2))
+    tI, xI = rows(rng, 2, 1, 64, BF16)
+    Q = torch.from_numpy(rng.standard_normal((L, 2, 4, 128)).astype(np.float32)).to(BF16)
+    qI = torch.from_numpy(rng.standard_normal((2, 4, 64)).astype(np.float32)).to(BF16).to(dev)
+    none = [None] * (L - 1)
+    O, idx = sa.decode_step_q8("FSS", [qI] + none, [torch.ones((2, 4), device=dev)] + none, [KI.pair()] + none,
+                               [C[k].pair() for k, _ in layers], [C[v].pair() for _, v in layers], i64(KI.off, dev),
+                               i32(new_lens, dev), 128, 40, Q.to(dev), Hkv, 0.1, out_dtype=F32,
+                               new_KI=[tI.to(dev)] + none, new_K=[t.to(dev) for t, _ in new_K],
+                               new_V=[t.to(dev) for t, _ in new_V])
+    first = {}
+    for l, pair in enumerate(layers):
+        for name, new in zip(pair, (new_K, new_V)):
+            first.setdefault(name, new[l][1])
+    for c, x in [(KI, xI)] + [(C[name], x) for name, x in first.items()]:
+        for b, n in enumerate(new_lens):
+            q8.append(c.codes[b], c.scales[b], x[b:b + 1], n)
+        c.check()
+    for l, (k, v) in enumerate(layers):
+        check_attn(Q[l:l + 1].float().numpy(), C[k], C[v], new_lens, idx.cpu().numpy(), Hkv, np.float32(0.1),
+                   O[l:l + 1], F32)
