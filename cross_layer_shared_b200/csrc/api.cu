@@ -1276,6 +1276,10 @@ sa_status validate_q8(const void* K8, const float* Ks, const void* V8, const flo
 }
 
 bool q8_width(int d) { return d == 64 || d == 128 || d == 192 || d == 256; }
+
+// Token places and index entries the attention counts in 32 bits, with room
+// for rounding up: 2^30 places are 256 GiB of codes.
+constexpr int64_t kAttnQ8MaxKeys = 1ll << 30;
 }  // namespace
 
 sa_status sa_cache_append_q8(const void* new_K, int64_t stride_K, const void* new_V, int64_t stride_V,
@@ -1390,7 +1394,7 @@ sa_status sa_index_score_q8(const void* qI, const float* w, const void* KI8, con
 size_t sa_decode_attn_q8_workspace_size(int L_g, int B, int64_t n_tokens, int S_max, int Hq, int Hkv, int d, int k) {
   (void)d;
   if (L_g < 1 || L_g > 4096 || B < 1 || B > 4096 || Hkv < 1 || Hq < Hkv || Hq / Hkv > 128 || k < 0 || S_max < 0 ||
-      n_tokens < 0 || (int64_t)L_g * B * Hq >= (1ll << 31))
+      n_tokens < 0 || n_tokens > kAttnQ8MaxKeys || k > kAttnQ8MaxKeys || (int64_t)L_g * B * Hq >= (1ll << 31))
     return SA_WS_HEADER_BYTES;  // the call itself refuses these
   return SA_WS_HEADER_BYTES + sa::attn_q8_scratch_bytes(sa::plan_attn_q8(L_g * (Hq / Hkv), B, Hkv, n_tokens, S_max, k,
                                                                          num_sms(), kSmallMaxCounters));
@@ -1409,6 +1413,8 @@ sa_status sa_decode_attn_q8(const void* Q, const void* K8, const float* K_scale,
   if (!V8 && n_tokens > 0) return fail(SA_ERR_INVALID_ARG, "%s: NULL pointer", who);
   sa_status st = validate_q8(K8, K_scale, V8, V_scale, seq_off, seq_len, B, n_tokens, Hkv, who);
   if (st != SA_OK) return st;
+  if (n_tokens > kAttnQ8MaxKeys || k > kAttnQ8MaxKeys)
+    return fail(SA_ERR_UNSUPPORTED, "%s: n_tokens=%lld and k=%d must be at most 2^30", who, (long long)n_tokens, k);
   if (Hq % Hkv != 0) return fail(SA_ERR_INVALID_ARG, "%s: Hq=%d not a multiple of Hkv=%d", who, Hq, Hkv);
   if (Hq / Hkv > 128) return fail(SA_ERR_UNSUPPORTED, "%s: Hq/Hkv=%d above 128", who, Hq / Hkv);
   if (out_dtype != SA_BF16 && out_dtype != SA_F32) return fail(SA_ERR_INVALID_ARG, "%s: bad out_dtype", who);

@@ -616,7 +616,8 @@ Split split_once(int64_t units, int64_t rounds, int sms, bool counters) {
 
 Q8AttnPlan plan_attn_q8(int R, int B, int Hkv, int64_t n_tokens, int S_max, int k, int sms, int max_counters) {
   Q8AttnPlan p;
-  const int64_t n = k > 0 ? k : S_max;  // keys of the longest unit
+  // keys of the longest unit (S_max may be a bound that bounds nothing)
+  const int64_t n = k > 0 ? k : S_max < n_tokens ? S_max : n_tokens;
   const int64_t rounds = n > kRound ? (n + kRound - 1) / kRound : 1;
   const int64_t slots = 2ll * sms;      // CTAs the GPU holds at once
   // More than 16 rows: 16 a CTA, K and V read again for every 16, where all
@@ -647,7 +648,6 @@ Q8AttnPlan plan_attn_q8(int R, int B, int Hkv, int64_t n_tokens, int S_max, int 
   if (chunk < least) chunk = least;
   chunk = (chunk + kRound - 1) / kRound * kRound;
   if (chunk < kRound) chunk = kRound;
-  if (chunk > 0x7fffff00) chunk = 0x7fffff00;
   p.chunk = (int)chunk;
   p.cluster = split.cluster;
   p.n_split = p.cluster ? (int)split.slices : (int)((n + chunk - 1) / chunk);

@@ -677,7 +677,7 @@ sa_status sa_index_score_q8(const void* qI, const float* w, const void* KI8, con
  * weights enter the second product with 22 bits or more for fp32 outputs, 8
  * or more (and divided by the sum of the rounded ones, or 11) for bf16
  * outputs.  A row with no token gets O = 0.  S_max >= every seq_len.  Supported: d = 128, Hq % Hkv ==
- * 0, Hq/Hkv <= 128.
+ * 0, Hq/Hkv <= 128, n_tokens and k at most 2^30.
  * Device errors: idx entry >= seq_len[b] -> SA_ERR_DEVICE, entry skipped.
  * Keys are split over several CTAs.  Where those are more than a cluster,
  * their partial results meet in the workspace (some counted in its header),

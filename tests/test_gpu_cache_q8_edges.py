@@ -106,3 +106,14 @@ def test_step_appends_to_every_listed_cache_once(layers, dev):
     for l, (k, v) in enumerate(layers):
         check_attn(Q[l:l + 1].float().numpy(), C[k], C[v], new_lens, idx.cpu().numpy(), Hkv, np.float32(0.1),
                    O[l:l + 1], F32)
+
+
+# ------------------------------------------------------------------ sizes at the ends
+@pytest.mark.parametrize("L,Hkv,lens", [(6, 80, [130]), (6, 80, [1000]), (1, 80, [300, 70]), (6, 2, [1500, 1])])
+def test_a_bound_that_bounds_nothing(L, Hkv, lens, dev):
+    """S_max = 2^31 - 1 only says that no length is longer."""
+    rng = np.random.default_rng(64)
+    K, V = filled(rng, lens, Hkv, 128, dev)
+    Qf = rng.standard_normal((L, len(lens), 4 * Hkv, 128))
+    attend(dev, K, V, lens, Qf, Hkv, S=2 ** 31 - 1)
+    attend(dev, K, V, lens, Qf, Hkv, picks(rng, lens, 100, 0.1), BF16, S=2 ** 31 - 1)
