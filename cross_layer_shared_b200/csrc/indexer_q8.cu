@@ -139,7 +139,7 @@ indexer_q8_kernel(const __grid_constant__ CUtensorMap tm_ki, const Q8IndexerArgs
       if (b < a.B) {
         const Q8Seq s = q8_seq(a.seq_off, a.seq_len, b, a.n_tokens, a.S_max);
         if (!s.ok && blockIdx.x == 0) report(a.status, kErrDevice, kKernIndexerQ8, b, a.seq_len[b], a.S_max);
-        n = (s.len + kTile - 1) / kTile;
+        n = q8_tiles(s.len, kTile);
       }
       int incl = n;
 #pragma unroll
@@ -246,7 +246,10 @@ indexer_q8_kernel(const __grid_constant__ CUtensorMap tm_ki, const Q8IndexerArgs
     bool fresh = true;
     Q8Seq seq = q8_seq(a.seq_off, a.seq_len, b, a.n_tokens, a.S_max);
     // scale of this thread's key of tile g of the sequence: loaded a tile ahead
-    auto key_scale = [&](int t) { return t < seq.len ? __ldcg(&a.scales[(seq.off + t) / kQ8Block]) : 0.f; };
+    // (unsigned: the tile ahead of a sequence's last may start at 2^31)
+    auto key_scale = [&](uint32_t t) {
+      return t < (uint32_t)seq.len ? __ldcg(&a.scales[(seq.off + t) / kQ8Block]) : 0.f;
+    };
     float ks = g_beg < g_end ? key_scale((g_beg - prefix[b]) * kTile + r) : 0.f;
     for (int g = g_beg, i = 0; g < g_end; ++g, ++i) {
       const int c = i % kAcc;
@@ -258,7 +261,7 @@ indexer_q8_kernel(const __grid_constant__ CUtensorMap tm_ki, const Q8IndexerArgs
         fresh = true;
       }
       const int t = (g - prefix[b]) * kTile + r;
-      const float ks_next = key_scale(t + kTile);
+      const float ks_next = key_scale((uint32_t)t + kTile);
       if (lane == 0) {
         if (fresh) {
           if (nseq > 0) mbar_arrive(&qempty[(nseq - 1) & 1]);
@@ -384,7 +387,7 @@ cudaError_t launch_nh(const Q8IndexerArgs& a, const CUtensorMap& tm_ki, int num_
   const size_t smem = Lay::smem_bytes(a.B, n_st);
   cudaError_t e = ensure_smem(kern, smem);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = (int64_t)a.B * ((a.S_max + kTile - 1) / kTile);
+  const int64_t tiles = (int64_t)a.B * q8_tiles(a.S_max, kTile);
   cudaLaunchConfig_t cfg = {};
   const int64_t ctas = (int64_t)num_sms * per_sm;
   cfg.gridDim = dim3((unsigned)(tiles < ctas ? tiles : ctas));

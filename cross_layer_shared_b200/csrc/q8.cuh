@@ -23,6 +23,12 @@ namespace sa {
 constexpr int kQ8Block = 64;
 constexpr uint32_t kQ8MinScaleBits = 1u << 23;  // 2^-126
 
+// tiles of `tile` tokens that hold len of them, for every len >= 0 an int holds
+__host__ __device__ constexpr int q8_tiles(int len, int tile) { return len / tile + (len % tile != 0); }
+static_assert(q8_tiles(0, 128) == 0 && q8_tiles(1, 128) == 1 && q8_tiles(128, 128) == 1 && q8_tiles(129, 128) == 2 &&
+                  q8_tiles(0x7fffffc0, 128) == 1 << 24,
+              "counted without passing 32 bits");
+
 // One sequence's place in the cache; ok is false (and the sequence counts as
 // empty) when the offsets do not describe one or len does not fit.
 struct Q8Seq {

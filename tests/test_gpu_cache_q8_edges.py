@@ -117,3 +117,42 @@ def test_a_bound_that_bounds_nothing(L, Hkv, lens, dev):
     Qf = rng.standard_normal((L, len(lens), 4 * Hkv, 128))
     attend(dev, K, V, lens, Qf, Hkv, S=2 ** 31 - 1)
     attend(dev, K, V, lens, Qf, Hkv, picks(rng, lens, 100, 0.1), BF16, S=2 ** 31 - 1)
+
+
+def test_index_keys_up_to_2_31(dev):
+    """One sequence of the most token places a cache may have: its last tokens appended, read back and scored."""
+    n, d, new = (1 << 31) - 64, 64, 100
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 152 << 30:
+        pytest.skip("137 GB of codes, 9 GB of scores and room to compare them")
+    rng = np.random.default_rng(65)
+    raw = torch.zeros((n, d), dtype=torch.uint8, device=dev)
+    K8 = raw.view(torch.float8_e4m3fn)
+    Ks = torch.ones(n // 64, device=dev)
+    off, ws = i64([0, n], dev), sa.workspace(sa.WS_HEADER_BYTES, dev)
+    q = torch.from_numpy(rng.standard_normal((1, 4, d)).astype(np.float32)).to(BF16)
+    w = torch.ones((1, 4))
+    scores = torch.full((1, n), 7.0, device=dev)
+    for length in (n - 5, n - 64):  # the last tile part full, and a length of whole tiles
+        t, x = rows(rng, new, 1, d, BF16)
+        first = length - new
+        codes, scales = np.zeros((1, 256, d), np.uint8), np.ones((1, 4))  # the last 256 places
+        raw[n - 256:] = 0
+        Ks[-4:] = 1
+        sa.cache_append_q8(t.to(dev), None, K8, Ks, None, None, off, i32([length], dev), i64([0, new], dev), ws=ws)
+        q8.append(codes, scales, x, length - (n - 256))
+        k = q8.values(codes, scales)[0]
+        back = sa.cache_read_q8(K8, Ks, None, None, off, i32([length], dev), n, 1,
+                                idx=i32([np.arange(first, length)], dev), out_dtype=F32, ws=ws)
+        assert np.array_equal(back[0, 0].double().cpu().numpy(), k[first - (n - 256):length - (n - 256)])
+        scores.fill_(7.0)
+        sa.index_score_q8(q.to(dev), w.to(dev), K8, Ks, off, i32([length], dev), n, scores=scores, ws=ws)
+        ok(ws)
+        want, mag = q8.index_scores(q[0].float().numpy(), w[0].numpy(), k)
+        tol = 140 * 2.0 ** -23 * mag + np.abs(k).sum(1) * np.abs(q[0].float().numpy()).max(1).sum() * 2.0 ** -17
+        last = scores[0, n - 256:].double().cpu().numpy()
+        end = length - (n - 256)
+        assert (np.abs(last[:end] - want[:end]) <= tol[:end]).all() and (last[end:] == 7).all()
+        assert sum(int(torch.count_nonzero(scores[0, a:min(a + (1 << 28), n - 256)])) for a in range(0, n - 256, 1 << 28)) == 0
+    del raw, K8, Ks, scores
+    torch.cuda.empty_cache()
