@@ -1275,6 +1275,11 @@ sa_status validate_q8(const void* K8, const float* Ks, const void* V8, const flo
   return SA_OK;
 }
 
+bool overlap(const void* a, const void* b, size_t bytes) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return x < y + bytes && y < x + bytes;
+}
+
 bool q8_width(int d) { return d == 64 || d == 128 || d == 192 || d == 256; }
 
 // Token places and index entries the attention counts in 32 bits, with room
@@ -1304,6 +1309,10 @@ sa_status sa_cache_append_q8(const void* new_K, int64_t stride_K, const void* ne
   if (!new_K) return fail(SA_ERR_INVALID_ARG, "%s: NULL pointer", who);
   if (!aligned(new_K, 16) || !aligned(new_V, 16))
     return fail(SA_ERR_INVALID_ARG, "%s: new rows must be 16-byte aligned", who);
+  // K and V are written at the same time: one cache as both is a race
+  const size_t rows = (size_t)n_tokens * Hkv;
+  if (V8 && (overlap(K8, V8, rows * d) || overlap(K_scale, V_scale, rows / sa::kQ8Block * 4)))
+    return fail(SA_ERR_INVALID_ARG, "%s: K and V caches overlap (append to a shared cache as one tensor)", who);
   sa::Q8AppendArgs a{};
   a.rows[0] = new_K;
   a.rows[1] = new_V;

@@ -622,7 +622,8 @@ sa_status sa_combine_partials(const float* O_part, int64_t o_stride, const float
  *   new_K, new_V  bf16 or fp32 (in_dtype) [n_rows, Hkv, d], one row of heads
  *             per token, stride_K / stride_V elements apart (so they may be
  *             slices of a fused projection), 16-byte aligned; new_V and V8
- *             NULL: one tensor
+ *             NULL: one tensor (K8 and V8 must not overlap: a cache that is
+ *             both is appended to as one tensor)
  *   new_off   int64 [B+1] (device): sequence b's rows are new_off[b] ..
  *             new_off[b+1]-1 (n_b may be 0); NULL: one row per sequence
  *   max_new   host upper bound of n_b

@@ -1,5 +1,7 @@
 """The 8-bit cache calls where they are most easily wrong, without a GPU: plans
 and refusals of the C entry points, and what the Python calls do around them."""
+import ctypes
+
 import pytest
 import torch
 
@@ -18,3 +20,21 @@ def test_a_bound_that_bounds_nothing_plans_like_the_cache(lib, L, B, Hq, Hkv, n_
 def test_attention_refuses_more_keys_than_it_counts(lib, kw):
     assert attn(lib, **kw) == sa.SA_ERR_UNSUPPORTED
     assert b"2^30" in lib.sa_last_error()
+
+
+BASE = 0x7F0000100000
+CODES = 256 * 8 * 128  # of the default arguments
+SCALES = 256 * 8 // 64 * 4
+
+
+@pytest.mark.parametrize("kw", [dict(V8=0), dict(V8=16), dict(V8=CODES - 16), dict(V8=16 - CODES), dict(Vs=0), dict(Vs=SCALES - 4),
+                                dict(Vs=4 - SCALES)], ids=lambda kw: "-".join(f"{k}{v:+d}" for k, v in kw.items()))
+def test_append_refuses_one_cache_as_k_and_v(lib, kw):
+    """Both are written at the same time.  (Never launched: an overlap is refused.)"""
+    at = lambda x: ctypes.c_void_p(x)
+    args = dict(K8=at(BASE), V8=at(BASE + 4 * CODES), Ks=at(BASE - 0x10000), Vs=at(BASE - 0x8000))
+    for name, base in (("V8", BASE), ("Vs", BASE - 0x10000)):
+        if name in kw:
+            args[name] = at(base + kw[name])
+    assert append(lib, **args) == sa.SA_ERR_INVALID_ARG
+    assert b"overlap" in lib.sa_last_error()
