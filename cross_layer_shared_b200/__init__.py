@@ -5,11 +5,17 @@ Every step of the path runs in the CUDA kernels of ``csrc/``; PyTorch
 provides device memory and streams.  There is no CPU fallback: if the
 library is not built, every call raises.
 
+What a call allocates itself (outputs and a workspace that are not given) is
+allocated on the stream it runs on, as under torch.cuda.stream(stream).  A
+workspace of the call's own goes with it, and with it what the kernels report
+there: give ws to read it with read_status.
+
 Build:  python -m cross_layer_shared_b200.build
 """
 from __future__ import annotations
 
 import array
+import contextlib
 import ctypes
 import os
 from typing import List, Optional, Sequence
@@ -166,10 +172,26 @@ def _ws(ws: torch.Tensor) -> torch.Tensor:
     return _dev(ws, torch.uint8, "ws")
 
 
-def workspace(nbytes: int, device="cuda") -> torch.Tensor:
+def _on(stream):
+    """What is allocated inside belongs to `stream` (None: the current one): it
+    is zeroed there, before the call's kernels, and its memory is used again
+    only behind them."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else
+                             torch.cuda.ExternalStream(stream.cuda_stream))
+
+
+def _empty(stream, shape, dtype, device) -> torch.Tensor:
+    with _on(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def workspace(nbytes: int, device="cuda", stream=None) -> torch.Tensor:
     """A zeroed workspace (status block included) of at least nbytes."""
     n = max(int(nbytes), WS_HEADER_BYTES)
-    return torch.zeros(n, dtype=torch.uint8, device=device)
+    with _on(stream):
+        return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
 def read_status(ws: torch.Tensor, stream=None):
@@ -199,14 +221,14 @@ def index_score(qI, w, KI, seq_off, seq_len, S_max: int, scores=None, ld: Option
     _seqs(seq_off, seq_len, B)
     if scores is None:
         ld = int(ld if ld is not None else max(S_max, 1))
-        scores = torch.empty((B, ld), dtype=torch.float32, device=qI.device)
+        scores = _empty(stream, (B, ld), dtype=torch.float32, device=qI.device)
     else:
         have = _rows_out(scores, B, S_max, "scores")
         if ld is not None and int(ld) != have:
             raise ValueError(f"ld={ld} does not match scores of {have} columns")
         ld = have
     if ws is None:
-        ws = workspace(lib().sa_index_score_workspace_size(B), qI.device)
+        ws = workspace(lib().sa_index_score_workspace_size(B), qI.device, stream)
     _ws(ws)
     _check(lib().sa_index_score(_ptr(qI), _ptr(w), _ptr(KI), _ptr(seq_off), _ptr(seq_len), B, KI.shape[0], S_max,
                                 H_I, d_I, _ptr(scores), ld, _ptr(ws), ws.numel(), _stream(stream)))
@@ -220,14 +242,14 @@ def index_score_prefill(qI, w, KI, q_pos, max_pos: int, scores=None, ld: Optiona
     _out(q_pos, (Nq,), (torch.int32,), "q_pos")
     if scores is None:
         ld = int(ld if ld is not None else max_pos + 1)
-        scores = torch.empty((Nq, ld), dtype=torch.float32, device=qI.device)
+        scores = _empty(stream, (Nq, ld), dtype=torch.float32, device=qI.device)
     else:
         have = _rows_out(scores, Nq, max_pos + 1, "scores")
         if ld is not None and int(ld) != have:
             raise ValueError(f"ld={ld} does not match scores of {have} columns")
         ld = have
     if ws is None:
-        ws = workspace(lib().sa_index_score_prefill_workspace_size(Nq), qI.device)
+        ws = workspace(lib().sa_index_score_prefill_workspace_size(Nq), qI.device, stream)
     _ws(ws)
     _check(lib().sa_index_score_prefill(_ptr(qI), _ptr(w), _ptr(KI), _ptr(q_pos), Nq, KI.shape[0], max_pos, H_I,
                                         d_I, _ptr(scores), ld, _ptr(ws), ws.numel(), _stream(stream)))
@@ -246,11 +268,11 @@ def index_topk_prefill(qI, w, KI, q_pos, max_pos: int, k: int, idx=None, rows_pe
     _dev(qI, torch.bfloat16, "qI"), _dev(w, torch.float32, "w"), _dev(KI, torch.bfloat16, "KI")
     _out(q_pos, (Nq,), (torch.int32,), "q_pos")
     if idx is None:
-        idx = torch.empty((Nq, k), dtype=torch.int32, device=qI.device)
+        idx = _empty(stream, (Nq, k), dtype=torch.int32, device=qI.device)
     _out(idx, (Nq, k), (torch.int32,), "idx")
     S = KI.shape[0]
     if ws is None:
-        ws = workspace(index_topk_prefill_workspace_size(Nq, S, max_pos, k, rows_per_block), qI.device)
+        ws = workspace(index_topk_prefill_workspace_size(Nq, S, max_pos, k, rows_per_block), qI.device, stream)
     _ws(ws)
     _check(lib().sa_index_topk_prefill(_ptr(qI), _ptr(w), _ptr(KI), _ptr(q_pos), Nq, S, max_pos, H_I, d_I, k,
                                        int(rows_per_block), _ptr(idx), _ptr(ws), ws.numel(), _stream(stream)))
@@ -262,14 +284,14 @@ def topk(scores, n_valid, n_max: int, k: int, idx=None, top_scores=None, want_sc
     _rows_out(scores, Nq, n_max, "scores")
     _out(n_valid, (Nq,), (torch.int32,), "n_valid")
     if idx is None:
-        idx = torch.empty((Nq, k), dtype=torch.int32, device=scores.device)
+        idx = _empty(stream, (Nq, k), dtype=torch.int32, device=scores.device)
     _out(idx, (Nq, k), (torch.int32,), "idx")
     if want_scores and top_scores is None:
-        top_scores = torch.empty((Nq, k), dtype=torch.float32, device=scores.device)
+        top_scores = _empty(stream, (Nq, k), dtype=torch.float32, device=scores.device)
     if top_scores is not None:
         _out(top_scores, (Nq, k), (torch.float32,), "top_scores")
     if ws is None:
-        ws = workspace(lib().sa_topk_workspace_size(Nq, n_max, k), scores.device)
+        ws = workspace(lib().sa_topk_workspace_size(Nq, n_max, k), scores.device, stream)
     _ws(ws)
     _check(lib().sa_topk(_ptr(scores), ld, _ptr(n_valid), Nq, n_max, k, _ptr(idx), _ptr(top_scores), _ptr(ws),
                          ws.numel(), _stream(stream)))
@@ -285,13 +307,13 @@ def topk_dynamic(scores, n_valid, n_max: int, k_max: int, tau: float, idx=None, 
     _rows_out(scores, Nq, n_max, "scores")
     _out(n_valid, (Nq,), (torch.int32,), "n_valid")
     if idx is None:
-        idx = torch.empty((Nq, k_max), dtype=torch.int32, device=scores.device)
+        idx = _empty(stream, (Nq, k_max), dtype=torch.int32, device=scores.device)
     _out(idx, (Nq, k_max), (torch.int32,), "idx")
     if counts is None:
-        counts = torch.empty((Nq,), dtype=torch.int32, device=scores.device)
+        counts = _empty(stream, (Nq,), dtype=torch.int32, device=scores.device)
     _out(counts, (Nq,), (torch.int32,), "counts")
     if ws is None:
-        ws = workspace(lib().sa_topk_dynamic_workspace_size(Nq, n_max, k_max), scores.device)
+        ws = workspace(lib().sa_topk_dynamic_workspace_size(Nq, n_max, k_max), scores.device, stream)
     _ws(ws)
     _check(lib().sa_topk_dynamic(_ptr(scores), ld, _ptr(n_valid), Nq, n_max, k_max, float(tau), _ptr(idx),
                                  _ptr(counts), _ptr(ws), ws.numel(), _stream(stream)))
@@ -312,10 +334,10 @@ def sparse_decode_attn(Q, K, V, seq_off, seq_len, idx, Hkv: int, scale: float, o
     _out(idx, (B, k), (torch.int32,), "idx")
     _seqs(seq_off, seq_len, B)
     if O is None:
-        O = torch.empty((L, B, Hq, d), dtype=out_dtype, device=Q.device)
+        O = _empty(stream, (L, B, Hq, d), dtype=out_dtype, device=Q.device)
     _out(O, (L, B, Hq, d), (torch.bfloat16, torch.float32), "O")
     if ws is None:
-        ws = workspace(sparse_decode_attn_workspace_size(L, B, Hq, Hkv, d, k), Q.device)
+        ws = workspace(sparse_decode_attn_workspace_size(L, B, Hq, Hkv, d, k), Q.device, stream)
     _ws(ws)
     code = SA_F32 if O.dtype == torch.float32 else SA_BF16
     _check(lib().sa_sparse_decode_attn(_ptr(Q), _ptr(K), _ptr(V), _ptr(seq_off), _ptr(seq_len), _ptr(idx), L, B,
@@ -340,13 +362,13 @@ def sparse_decode_attn_partial(Q, K, V, seq_off, seq_len, idx, Hkv: int, scale: 
         _out(idx_count, (B,), (torch.int32,), "idx_count")
     _seqs(seq_off, seq_len, B)
     if O_part is None:
-        O_part = torch.empty((L, B, Hq, d), dtype=torch.float32, device=Q.device)
+        O_part = _empty(stream, (L, B, Hq, d), dtype=torch.float32, device=Q.device)
     if ml is None:
-        ml = torch.empty((L, B, Hq, 2), dtype=torch.float32, device=Q.device)
+        ml = _empty(stream, (L, B, Hq, 2), dtype=torch.float32, device=Q.device)
     _out(O_part, (L, B, Hq, d), (torch.float32,), "O_part")
     _out(ml, (L, B, Hq, 2), (torch.float32,), "ml")
     if ws is None:
-        ws = workspace(sparse_decode_attn_workspace_size(L, B, Hq, Hkv, d, k), Q.device)
+        ws = workspace(sparse_decode_attn_workspace_size(L, B, Hq, Hkv, d, k), Q.device, stream)
     _ws(ws)
     _check(lib().sa_sparse_decode_attn_partial(_ptr(Q), _ptr(K), _ptr(V), _ptr(seq_off), _ptr(seq_len), _ptr(idx),
                                                L, B, n_tokens, Hq, Hkv, d, k, _ptr(idx_count), float(scale),
@@ -374,12 +396,12 @@ def cp_select(cand_scores, cand_idx, rank: int, local_idx=None, local_count=None
             or cand_scores.stride()[1:] != (k, 1):
         raise ValueError("cand_scores and cand_idx must be [B, k] blocks of one rank stride")
     if local_idx is None:
-        local_idx = torch.empty((B, k), dtype=torch.int32, device=cand_idx.device)
+        local_idx = _empty(stream, (B, k), dtype=torch.int32, device=cand_idx.device)
     _out(local_idx, (B, k), (torch.int32,), "local_idx")
     if local_count is not None:
         _out(local_count, (B,), (torch.int32,), "local_count")
     if ws is None:
-        ws = workspace(cp_select_workspace_size(N, B, k), cand_idx.device)
+        ws = workspace(cp_select_workspace_size(N, B, k), cand_idx.device, stream)
     _ws(ws)
     _check(lib().sa_cp_select(_ptr(cand_scores), _ptr(cand_idx), stride, N, B, k, int(rank), _ptr(local_idx),
                               _ptr(local_count), _ptr(ws), ws.numel(), _stream(stream)))
@@ -419,7 +441,7 @@ def cp_radix_level(scores, n_local, k: int, N: int, level: int, gathered=None, h
         raise ValueError("gathered histograms are needed at levels 1 and 2 only")
     g, stride = _gathered(gathered, N, B, RADIX_BINS[level - 1], "cp_radix_level") if level else (None, 0)
     if hist_out is None:
-        hist_out = torch.empty((B, RADIX_BINS[level]), dtype=torch.int32, device=scores.device)
+        hist_out = _empty(stream, (B, RADIX_BINS[level]), dtype=torch.int32, device=scores.device)
     _out(hist_out, (B, RADIX_BINS[level]), (torch.int32,), "hist_out")
     if ws is None:
         raise ValueError("cp_radix_level needs the step's workspace (it carries the state across levels)")
@@ -440,7 +462,7 @@ def cp_radix_select(scores, n_local, k: int, N: int, rank: int, gathered, local_
     _dev(n_local, torch.int32, "n_local")
     g, stride = _gathered(gathered, N, B, RADIX_BINS[2], "cp_radix_select")
     if local_idx is None:
-        local_idx = torch.empty((B, k), dtype=torch.int32, device=scores.device)
+        local_idx = _empty(stream, (B, k), dtype=torch.int32, device=scores.device)
     _out(local_idx, (B, k), (torch.int32,), "local_idx")
     if local_count is not None:
         _out(local_count, (B,), (torch.int32,), "local_count")
@@ -464,7 +486,7 @@ def combine_partials(O_part, ml, O=None, out_dtype=torch.bfloat16, stream=None) 
     if O_part.stride()[1:] != (d, 1) or ml.stride()[1:] != (2, 1):
         raise ValueError("each part of O_part and ml must be contiguous")
     if O is None:
-        O = torch.empty((rows, d), dtype=out_dtype, device=O_part.device)
+        O = _empty(stream, (rows, d), dtype=out_dtype, device=O_part.device)
     _out(O, (rows, d), (torch.bfloat16, torch.float32), "O")
     code = SA_F32 if O.dtype == torch.float32 else SA_BF16
     _check(lib().sa_combine_partials(_ptr(O_part), O_part.stride(0), _ptr(ml), ml.stride(0), P, rows, d, _ptr(O),
@@ -487,13 +509,13 @@ def indexer_layer_attn(Q, K, V, seq_off, seq_len, S_max: int, Hkv: int, scale: f
     _dev(Q, torch.bfloat16, "Q"), _dev(K, torch.bfloat16, "K"), _dev(V, torch.bfloat16, "V")
     _seqs(seq_off, seq_len, B)
     if O is None:
-        O = torch.empty((B, Hq, d), dtype=out_dtype, device=Q.device)
+        O = _empty(stream, (B, Hq, d), dtype=out_dtype, device=Q.device)
     _out(O, (B, Hq, d), (torch.bfloat16, torch.float32), "O")
     if scores is None:
-        scores = torch.empty((B, max(S_max, 1)), dtype=torch.float32, device=Q.device)
+        scores = _empty(stream, (B, max(S_max, 1)), dtype=torch.float32, device=Q.device)
     ld = _rows_out(scores, B, S_max, "scores")
     if ws is None:
-        ws = workspace(indexer_layer_attn_workspace_size(B, S_max, Hq, Hkv, d), Q.device)
+        ws = workspace(indexer_layer_attn_workspace_size(B, S_max, Hq, Hkv, d), Q.device, stream)
     _ws(ws)
     code = SA_F32 if O.dtype == torch.float32 else SA_BF16
     _check(lib().sa_indexer_layer_attn(_ptr(Q), _ptr(K), _ptr(V), _ptr(seq_off), _ptr(seq_len), B, n_tokens, S_max,
@@ -520,9 +542,9 @@ def decode_step_attn_route(Q, K, V, seq_off, seq_len, S_max: int, k: int, Hkv: i
     index is then -1 padded and (O, idx, counts) is returned."""
     L, B, Hq, d = Q.shape
     if O is None:
-        O = torch.empty((L, B, Hq, d), dtype=out_dtype, device=Q.device)
+        O = _empty(stream, (L, B, Hq, d), dtype=out_dtype, device=Q.device)
     if ws is None:
-        ws = workspace(decode_step_attn_route_workspace_size(B, S_max, Hq, Hkv, d, k, L), Q.device)
+        ws = workspace(decode_step_attn_route_workspace_size(B, S_max, Hq, Hkv, d, k, L), Q.device, stream)
     _, scores = indexer_layer_attn(Q[0], K, V, seq_off, seq_len, S_max, Hkv, scale, O=O[0], scores=scores, ws=ws,
                                    stream=stream)
     if tau is None:
@@ -585,16 +607,16 @@ def decode_step(pattern: str, qI: Sequence, w: Sequence, KI: Sequence, K: Sequen
     _dev(Q, torch.bfloat16, "Q")
     _seqs(seq_off, seq_len, B)
     if O is None:
-        O = torch.empty((L, B, Hq, d), dtype=out_dtype, device=Q.device)
+        O = _empty(stream, (L, B, Hq, d), dtype=out_dtype, device=Q.device)
     _out(O, (L, B, Hq, d), (torch.bfloat16, torch.float32), "O")
     if idx is None:
-        idx = torch.empty((B, k), dtype=torch.int32, device=Q.device)
+        idx = _empty(stream, (B, k), dtype=torch.int32, device=Q.device)
     _out(idx, (B, k), (torch.int32,), "idx")
     if scores is None:
-        scores = torch.empty((B, max(S_max, 1)), dtype=torch.float32, device=Q.device)
+        scores = _empty(stream, (B, max(S_max, 1)), dtype=torch.float32, device=Q.device)
     _rows_out(scores, B, S_max, "scores")
     if ws is None:
-        ws = workspace(decode_step_workspace_size(n, B, S_max, Hq, Hkv, d, k), Q.device)
+        ws = workspace(decode_step_workspace_size(n, B, S_max, Hq, Hkv, d, k), Q.device, stream)
     _ws(ws)
     code = SA_F32 if O.dtype == torch.float32 else SA_BF16
     if new_KI is None and new_K is None and not per_layer:
@@ -672,16 +694,16 @@ def block_union_prefill(idx, q_pos, Q, K, V, block: int, scale: float, out_dtype
     _dev(Q, torch.bfloat16, "Q"), _dev(K, torch.bfloat16, "K"), _dev(V, torch.bfloat16, "V")
     nb = (S + block - 1) // block
     if kv_indptr is None:
-        kv_indptr = torch.empty(Hkv + 1, dtype=torch.int32, device=Q.device)
+        kv_indptr = _empty(stream, Hkv + 1, dtype=torch.int32, device=Q.device)
     _out(kv_indptr, (Hkv + 1,), (torch.int32,), "kv_indptr")
     if kv_indices is None:
-        kv_indices = torch.empty(Hkv * nb, dtype=torch.int32, device=Q.device)
+        kv_indices = _empty(stream, Hkv * nb, dtype=torch.int32, device=Q.device)
     _out(kv_indices, (Hkv * nb,), (torch.int32,), "kv_indices")
     if O is None:
-        O = torch.empty((Nq, Hq, d), dtype=out_dtype, device=Q.device)
+        O = _empty(stream, (Nq, Hq, d), dtype=out_dtype, device=Q.device)
     _out(O, (Nq, Hq, d), (torch.bfloat16, torch.float32), "O")
     if ws is None:
-        ws = workspace(lib().sa_block_union_prefill_workspace_size(S, Nq, Hq, Hkv, d, k, block), Q.device)
+        ws = workspace(lib().sa_block_union_prefill_workspace_size(S, Nq, Hq, Hkv, d, k, block), Q.device, stream)
     _ws(ws)
     code = SA_F32 if O.dtype == torch.float32 else SA_BF16
     _check(lib().sa_block_union_prefill(_ptr(idx), _ptr(q_pos), _ptr(Q), _ptr(K), _ptr(V), S, Nq, Hq, Hkv, d, k,
@@ -710,10 +732,10 @@ def kap_order(idx, S: int, block: int, q_block: int, kv_indptr, kv_indices, orde
     _out(kv_indptr, (kv_indptr.numel(),), (torch.int32,), "kv_indptr")
     _out(kv_indices, (kv_indices.numel(),), (torch.int32,), "kv_indices")
     if order is None:
-        order = torch.empty((n_qb, nb), dtype=torch.int32, device=idx.device)
+        order = _empty(stream, (n_qb, nb), dtype=torch.int32, device=idx.device)
     _out(order, (n_qb, nb), (torch.int32,), "order")
     if ws is None:
-        ws = workspace(lib().sa_kap_order_workspace_size(), idx.device)
+        ws = workspace(lib().sa_kap_order_workspace_size(), idx.device, stream)
     _ws(ws)
     _check(lib().sa_kap_order(_ptr(idx), Nq, k, S, block, q_block, _ptr(kv_indptr), _ptr(kv_indices), _ptr(order),
                               nb, _ptr(ws), ws.numel(), _stream(stream)))
@@ -737,22 +759,22 @@ def osk_prefill(idx, q_pos, Q, K, V, block: int, scale: float, tau: float, out_d
     n_qb = (Nq * G + 127) // 128
     dev = Q.device
     if kv_indptr is None:
-        kv_indptr = torch.empty(Hkv + 1, dtype=torch.int32, device=dev)
+        kv_indptr = _empty(stream, Hkv + 1, dtype=torch.int32, device=dev)
     _out(kv_indptr, (Hkv + 1,), (torch.int32,), "kv_indptr")
     if kv_indices is None:
-        kv_indices = torch.empty(Hkv * nb, dtype=torch.int32, device=dev)
+        kv_indices = _empty(stream, Hkv * nb, dtype=torch.int32, device=dev)
     _out(kv_indices, (Hkv * nb,), (torch.int32,), "kv_indices")
     if order is None:
-        order = torch.empty((n_qb, nb), dtype=torch.int32, device=dev)
+        order = _empty(stream, (n_qb, nb), dtype=torch.int32, device=dev)
     _out(order, (n_qb, nb), (torch.int32,), "order")
     if steps is None:
-        steps = torch.empty(Hkv * n_qb, dtype=torch.int32, device=dev)
+        steps = _empty(stream, Hkv * n_qb, dtype=torch.int32, device=dev)
     _out(steps, (Hkv * n_qb,), (torch.int32,), "steps")
     if O is None:
-        O = torch.empty((Nq, Hq, d), dtype=out_dtype, device=dev)
+        O = _empty(stream, (Nq, Hq, d), dtype=out_dtype, device=dev)
     _out(O, (Nq, Hq, d), (torch.bfloat16, torch.float32), "O")
     if ws is None:
-        ws = workspace(lib().sa_osk_prefill_workspace_size(S, Nq, Hq, Hkv, d, k, block), dev)
+        ws = workspace(lib().sa_osk_prefill_workspace_size(S, Nq, Hq, Hkv, d, k, block), dev, stream)
     _ws(ws)
     code = SA_F32 if O.dtype == torch.float32 else SA_BF16
     _check(lib().sa_osk_prefill(_ptr(idx), _ptr(q_pos), _ptr(Q), _ptr(K), _ptr(V), S, Nq, Hq, Hkv, d, k, block,
@@ -822,7 +844,7 @@ def cache_append_q8(new_K, new_V, K8, K_scale, V8, V_scale, seq_off, seq_len, ne
     seq_len already counts them.  max_new: host bound of a sequence's new
     rows (default: n).  One tensor: new_V = V8 = V_scale = None."""
     if ws is None:
-        ws = workspace(WS_HEADER_BYTES, K8.device)
+        ws = workspace(WS_HEADER_BYTES, K8.device, stream)
     code = (_native or _q8()).cache_append_q8(new_K, new_V, K8, K_scale, V8, V_scale, seq_off, seq_len, new_off,
                                               max_new, ws, _raw(stream))
     if code:
@@ -848,11 +870,11 @@ def cache_read_q8(K8, K_scale, V8, V_scale, seq_off, seq_len, S_max: int, Hkv: i
                 n_out = K.numel() // max(Hkv * d, 1)
             shape = (n_out * Hkv, d)
         if K is None:
-            K = torch.empty(shape, dtype=out_dtype, device=K8.device)
+            K = _empty(stream, shape, dtype=out_dtype, device=K8.device)
         if V is None and V8 is not None:
-            V = torch.empty(shape, dtype=K.dtype, device=K8.device)
+            V = _empty(stream, shape, dtype=K.dtype, device=K8.device)
     if ws is None:
-        ws = workspace(WS_HEADER_BYTES, K8.device)
+        ws = workspace(WS_HEADER_BYTES, K8.device, stream)
     code = (_native or _q8()).cache_read_q8(K8, K_scale, V8, V_scale, seq_off, seq_len, S_max, Hkv, idx, out_off,
                                             n_out, K, V, ws, _raw(stream))
     if code:
@@ -864,12 +886,12 @@ def index_score_q8(qI, w, KI8, KI_scale, seq_off, seq_len, S_max: int, scores=No
                    stream=None) -> torch.Tensor:
     """index_score over an 8-bit key cache (sa_index_score_q8)."""
     if scores is None:
-        scores = torch.empty((qI.shape[0], int(ld if ld is not None else max(S_max, 1))), dtype=torch.float32,
+        scores = _empty(stream, (qI.shape[0], int(ld if ld is not None else max(S_max, 1))), dtype=torch.float32,
                              device=qI.device)
     elif ld is not None and ld != scores.shape[-1]:
         raise ValueError(f"ld={ld} does not match scores of {scores.shape[-1]} columns")
     if ws is None:
-        ws = workspace(WS_HEADER_BYTES, qI.device)
+        ws = workspace(WS_HEADER_BYTES, qI.device, stream)
     code = (_native or _q8()).index_score_q8(qI, w, KI8, KI_scale, seq_off, seq_len, S_max, scores, ws, _raw(stream))
     if code:
         _check(code)
@@ -886,11 +908,11 @@ def decode_attn_q8(Q, K8, K_scale, V8, V_scale, seq_off, seq_len, S_max: int, Hk
     Hq, d] over the tokens of idx int32 [B, k] (shared by the L layers), or
     with idx None over every token of each sequence.  Returns O [L, B, Hq, d]."""
     if O is None:
-        O = torch.empty(Q.shape, dtype=out_dtype, device=Q.device)
+        O = _empty(stream, Q.shape, dtype=out_dtype, device=Q.device)
     if ws is None:
         L, B, Hq, d = Q.shape
         ws = workspace(decode_attn_q8_workspace_size(L, B, K8.numel() // max(Hkv * d, 1), S_max, Hq, Hkv, d,
-                                                     0 if idx is None else idx.shape[-1]), Q.device)
+                                                     0 if idx is None else idx.shape[-1]), Q.device, stream)
     code = (_native or _q8()).decode_attn_q8(Q, K8, K_scale, V8, V_scale, seq_off, seq_len, S_max, Hkv, scale, idx, O,
                                              ws, _raw(stream))
     if code:
@@ -928,14 +950,14 @@ def decode_step_q8(pattern: str, qI: Sequence, w: Sequence, KI: Sequence, K: Seq
     if any(x is not None and len(x) != n for x in (new_KI, new_K, new_V)):
         raise ValueError("new rows must be listed per layer")
     if O is None:
-        O = torch.empty((L, B, Hq, d), dtype=out_dtype, device=Q.device)
+        O = _empty(stream, (L, B, Hq, d), dtype=out_dtype, device=Q.device)
     if idx is None:
-        idx = torch.empty((B, k), dtype=torch.int32, device=Q.device)
+        idx = _empty(stream, (B, k), dtype=torch.int32, device=Q.device)
     if scores is None:
-        scores = torch.empty((B, max(S_max, 1)), dtype=torch.float32, device=Q.device)
+        scores = _empty(stream, (B, max(S_max, 1)), dtype=torch.float32, device=Q.device)
     if ws is None:
         n_tokens = K[0][0].numel() // (Hkv * d)
-        ws = workspace(decode_step_q8_workspace_size(n, B, n_tokens, S_max, Hq, Hkv, d, k), Q.device)
+        ws = workspace(decode_step_q8_workspace_size(n, B, n_tokens, S_max, Hq, Hkv, d, k), Q.device, stream)
     done = set()  # caches that hold the new rows
 
     def first(cache) -> bool:

@@ -1,6 +1,8 @@
 """The 8-bit cache calls where they are most easily wrong, without a GPU: plans
 and refusals of the C entry points, and what the Python calls do around them."""
+import ast
 import ctypes
+import inspect
 
 import pytest
 import torch
@@ -38,3 +40,70 @@ def test_append_refuses_one_cache_as_k_and_v(lib, kw):
             args[name] = at(base + kw[name])
     assert append(lib, **args) == sa.SA_ERR_INVALID_ARG
     assert b"overlap" in lib.sa_last_error()
+
+
+class Side:
+    """A stream of another library's: its address is all there is."""
+    cuda_stream = 1234
+
+
+def test_what_a_call_allocates_belongs_to_its_stream(monkeypatch):
+    """Outputs, temporaries and workspaces that are not given are allocated (and zeroed) on the stream of the call."""
+    on, made = [], []
+    bf, f8 = torch.bfloat16, torch.float8_e4m3fn
+    c, s = torch.zeros((128, 128), dtype=f8), torch.ones(2)
+    off, ln = torch.tensor([0, 128]), torch.tensor([5], dtype=torch.int32)
+    Q, q, w, x = torch.zeros((1, 1, 4, 128), dtype=bf), torch.zeros((1, 4, 128), dtype=bf), torch.ones((1, 4)), torch.zeros((1, 1, 128))
+
+    class Stream:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            on.append(self.stream)
+
+        def __exit__(self, *a):
+            on.pop()
+
+    def recording(make):
+        def f(*a, **kw):
+            made.append(on[-1] if on else None)
+            return make(*a, **{**kw, "device": "cpu"})
+        return f
+
+    class Native:  # the compiled marshalling: every call succeeds
+        def __getattr__(self, name):
+            return lambda *a: 0
+
+    monkeypatch.setattr(sa, "_native", Native())
+    monkeypatch.setattr(sa, "topk", lambda *a, **kw: None)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda p: ("stream at", p))
+    monkeypatch.setattr(torch.cuda, "stream", Stream)
+    monkeypatch.setattr(torch, "empty", recording(torch.empty))
+    monkeypatch.setattr(torch, "zeros", recording(torch.zeros))
+    calls = {
+        1: lambda **kw: sa.cache_append_q8(x, None, c, s, None, None, off, ln, **kw),
+        3: lambda **kw: sa.cache_read_q8(c, s, c, s, off, ln, 128, 1, out_off=off, n_out=128, **kw),
+        2: lambda **kw: sa.index_score_q8(q, w, c, s, off, ln, 128, **kw),
+        -2: lambda **kw: sa.decode_attn_q8(Q, c, s, c, s, off, ln, 128, 1, 0.1, **kw),
+        4: lambda **kw: sa.decode_step_q8("F", [q], [w], [(c, s)], [(c, s)], [(c, s)], off, ln, 128, 16, Q, 1, 0.1, **kw),
+    }
+    for n, call in calls.items():
+        for kw, want in ((dict(stream=Side()), ("stream at", 1234)), (dict(), None)):
+            made.clear()
+            call(**kw)
+            assert made == [want] * abs(n)
+
+
+def test_every_call_with_a_stream_allocates_there():
+    for name, f in vars(sa).items():
+        if callable(f) and not isinstance(f, type) and name not in ("_empty", "workspace") and f.__module__ == sa.__name__ \
+                and "stream" in inspect.signature(f).parameters:
+            text = inspect.getsource(f)
+            assert "torch.empty(" not in text and "torch.zeros(" not in text, name
+            made = ast.walk(ast.parse(text))
+            for call in (c for c in made if isinstance(c, ast.Call) and isinstance(c.func, ast.Name)):
+                if call.func.id == "_empty":
+                    assert getattr(call.args[0], "id", None) == "stream", name
+                if call.func.id == "workspace":
+                    assert getattr(call.args[-1], "id", None) == "stream", name

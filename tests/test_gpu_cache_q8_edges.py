@@ -156,3 +156,41 @@ def test_index_keys_up_to_2_31(dev):
         assert sum(int(torch.count_nonzero(scores[0, a:min(a + (1 << 28), n - 256)])) for a in range(0, n - 256, 1 << 28)) == 0
     del raw, K8, Ks, scores
     torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------------ another stream, without a workspace
+def test_calls_on_another_stream_with_memory_of_their_own(dev):
+    """The current stream is busy and has just given back memory full of ones: a call on another stream neither waits
+    for it nor reads that memory as its workspace."""
+    rng = np.random.default_rng(67)
+    lens = [9000, 500]
+    K, V = filled(rng, lens, 2, 128, dev)
+    KI, _ = filled(rng, lens, 1, 64, dev)
+    off, ln = i64(K.off, dev), i32(lens, dev)
+    bf = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32)).to(dev).to(BF16)
+    Q, qI, w = bf(1, 2, 8, 128), bf(2, 4, 64), torch.rand((2, 4), device=dev)
+    packed = i64([0, 9000, 9500], dev)
+    Kb, Vb = sa.cache_read_q8(*K.pair(), *V.pair(), off, ln, 9000, 2, out_off=packed, n_out=9500)
+
+    def calls(**kw):
+        scores = sa.index_score_q8(qI, w, *KI.pair(), off, ln, 9000, **kw)
+        with torch.cuda.stream(kw.get("stream")):
+            scores[1, 500:] = 0  # not written
+        idx = sa.topk(scores, ln, 9000, 256, **kw)
+        return (scores, idx, sa.decode_attn_q8(Q, *K.pair(), *V.pair(), off, ln, 9000, 2, 0.1, out_dtype=F32, **kw),
+                sa.decode_attn_q8(Q, *K.pair(), *V.pair(), off, ln, 9000, 2, 0.1, idx=idx, **kw),
+                *sa.cache_read_q8(*K.pair(), *V.pair(), off, ln, 9000, 2, idx=idx, **kw),
+                sa.sparse_decode_attn(Q, Kb, Vb, packed, ln, idx, 2, 0.1, out_dtype=F32, **kw))
+
+    want = calls()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    calls(stream=side)  # memory of the stream's own to use again
+    for _ in range(4):
+        torch.cuda.synchronize()
+        torch.cuda._sleep(50_000_000)
+        for n in (4096, 1 << 16, 1 << 20):
+            torch.full((n,), 255, dtype=torch.uint8, device=dev)
+        got = calls(stream=side)
+        side.synchronize()
+        assert all(torch.equal(a.cpu(), b.cpu()) for a, b in zip(want, got))
