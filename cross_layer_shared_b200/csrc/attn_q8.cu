@@ -636,8 +636,12 @@ Q8AttnPlan plan_attn_q8(int R, int B, int Hkv, int64_t n_tokens, int S_max, int 
   }
   p.rows = R <= 8 ? 8 : 16;
   // Much work (from 2048 keys per slot): about four slices per slot, so that
-  // ragged sequences and the last wave even out.
-  const int64_t keys = (k > 0 ? (int64_t)B * k : n_tokens) * Hkv * p.row_tiles;
+  // ragged sequences and the last wave even out.  What counts is the keys there
+  // can be, not the cache's places: a cache with room to grow may hold short
+  // sequences.
+  int64_t keys = B * n;
+  if (k == 0 && keys > n_tokens) keys = n_tokens;
+  keys *= (int64_t)Hkv * p.row_tiles;
   int64_t chunk = (n + split.slices - 1) / split.slices;
   if (keys >= slots * 2048) {
     split.cluster = 0;

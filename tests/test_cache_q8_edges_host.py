@@ -107,3 +107,11 @@ def test_every_call_with_a_stream_allocates_there():
                     assert getattr(call.args[0], "id", None) == "stream", name
                 if call.func.id == "workspace":
                     assert getattr(call.args[-1], "id", None) == "stream", name
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,S_max", [(1, 64, 8, 8192), (4, 32, 8, 4096), (2, 8, 1, 1000)])
+def test_room_to_grow_does_not_change_the_plan(lib, B, Hq, Hkv, S_max):
+    """The split goes by the keys there can be (S_max of each sequence), not by the cache's token places."""
+    size = sa.decode_attn_q8_workspace_size
+    tight = B * (S_max + 63) // 64 * 64
+    assert size(1, B, 1 << 20, S_max, Hq, Hkv, 128, 0) == size(1, B, tight, S_max, Hq, Hkv, 128, 0)
