@@ -25,17 +25,20 @@
 //     from ldmatrix.trans on pairs of codes: a lane gets two dims of two keys,
 //     one byte permute turns that into two operand registers' worth of codes.
 //   * P^T's operand layout is one movmatrix away from S^T's accumulators.  For
-//     fp32 outputs P is split into two halves (22 bits); for bf16 outputs one
-//     half (11 bits, eight times finer than the output's rounding).
+//     fp32 outputs P is split into two halves (22 bits, down to 2^-10 of the
+//     row's largest); for bf16 outputs one half (11 bits, eight times finer
+//     than the output's rounding).
 //   * The V scale vs = f 2^e (f = 1 for the powers of two an append writes)
 //     joins the logit: o sums f 2^(z + e - m_o) cv with a reference m_o over
 //     z + e of its own, l sums 2^(z - m_l).  So a key's weight is held
 //     relative to the largest contribution, however far the scales are apart.
 //   * m_o moves only when some key passes it by more than 14 (log2 units) and
 //     is then set 7 below the maximum: weights, f < 2 included, stay below
-//     2^15 and most of f16's range is above its subnormals (a weight times its
-//     V scale keeps its bits down to 2^-21 of the row's largest, and one of
-//     2^-32 is lost).  l is a float: m_l moves past 60.
+//     2^15 and most of f16's range is above its subnormals: a weight times its
+//     V scale keeps a half's 11 bits down to 2^-21 of the row's largest, is off
+//     by at most 2^-32 of that in one half or two (f16's last subnormal bit,
+//     2^-24, where the largest is 2^7 or more), and one below that is lost.  l
+//     is a float: m_l moves past 60.
 //   * Padding entries and tokens past the length have codes zero and weight
 //     zero, whatever the cache holds there.
 //   * Partial results travel normalised: (m, l, o / l).  A weighted mean of V

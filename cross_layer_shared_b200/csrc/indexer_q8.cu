@@ -7,8 +7,10 @@
 // are: tcgen05 kind::f8f6f4 multiplies e4m3 by e4m3, so only the bf16 queries
 // have to change.  Each query row is scaled by a power of two into (224, 448]
 // and split into two e4m3 parts, hi + lo: a bf16 element has 8 significant
-// bits and each part holds 4, so the split is exact down to 2^-11 of the row's
-// largest element, and below it is off by less than 2^-17 of that element.
+// bits and each part holds 4.  lo's smallest step is 2^-9, the last bit of an
+// element of 2^-2, so the split is exact down to 2^-9 of the row's largest
+// element (over all mantissas: down to 2^-9.8), and below it is off by less
+// than 2^-17 of that element.
 // Both parts are columns of one B operand, so a key tile is read from shared
 // memory once for them; the epilogue adds the two columns of a head.
 //

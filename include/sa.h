@@ -660,7 +660,7 @@ sa_status sa_cache_read_q8(const void* K8, const float* K_scale, const void* V8,
  *   scores[b*ld + t] = sum_j w[b,j] * max(0, sum_c qI[b,j,c] * KI[seq_off[b]+t, c])
  * for t in [0, seq_len[b]), fp32 accumulation, canonical +0; entries t >=
  * seq_len[b] are left untouched.  The queries stay bf16 (finite): they enter
- * the products as two e4m3 parts, exact but for elements below 2^-11 of their
+ * the products as two e4m3 parts, exact but for elements below 2^-9 of their
  * row's largest, which are off by at most 2^-17 of it.
  * A product that is NaN (a NaN code) counts as 0, as in
  * sa_index_score.  Supported: 1 <= H_I <= 64, d_I in {64, 128, 192, 256}. */
@@ -675,10 +675,12 @@ sa_status sa_index_score_q8(const void* qI, const float* w, const void* KI8, con
  * over the tokens of idx[b,:] (entries < 0 skipped, a token listed twice
  * counts twice), or with idx = NULL and k = 0 over every token t <
  * seq_len[b] (a dense layer).  Softmax sums and accumulation are fp32; the
- * weights enter the second product with 22 bits or more for fp32 outputs, 8
- * or more (and divided by the sum of the rounded ones, or 11) for bf16
- * outputs.  A row with no token gets O = 0.  S_max >= every seq_len.  Supported: d = 128, Hq % Hkv ==
- * 0, Hq/Hkv <= 128, n_tokens and k at most 2^30.
+ * weights enter the second product with 22 bits or more for fp32 outputs
+ * (what is below 2^-10 of the row's largest weight, V's scales included, may
+ * be off by 2^-32 of that one instead), 8 or more (and divided by the sum of
+ * the rounded ones, or 11) for bf16 outputs.  A row with no token gets O = 0.
+ * S_max >= every seq_len.  Supported: d = 128, Hq % Hkv == 0, Hq/Hkv <= 128,
+ * n_tokens and k at most 2^30.
  * Device errors: idx entry >= seq_len[b] -> SA_ERR_DEVICE, entry skipped.
  * Keys are split over several CTAs.  Where those are more than a cluster,
  * their partial results meet in the workspace (some counted in its header),

@@ -194,3 +194,25 @@ def test_calls_on_another_stream_with_memory_of_their_own(dev):
         got = calls(stream=side)
         side.synchronize()
         assert all(torch.equal(a.cpu(), b.cpu()) for a, b in zip(want, got))
+
+
+# ------------------------------------------------------------------ the queries' two parts
+def test_index_queries_keep_what_is_promised_of_them(dev):
+    """One-hot keys give the query elements back: exact down to 2^-9 of their row's largest, and off by at most
+    2^-17 of it below, for every mantissa of the largest and elements of 14 binades."""
+    rng = np.random.default_rng(66)
+    B, d = 128, 128
+    C = Cache([128] * B, 1, d, dev, fill=0)
+    for b in range(B):
+        C.codes[b][0][np.arange(d), np.arange(d)] = 0x38  # 1.0
+        C.scales[b][:] = 1.0
+    C.upload()
+    q = (1 + np.arange(128) / 128)[:, None] * np.ones((1, d))
+    q[:, 1:] = (1 + rng.integers(0, 128, (B, d - 1)) / 128) * np.exp2(-1.0 - rng.integers(0, 14, (B, d - 1)))
+    qt = torch.from_numpy(q.astype(np.float32)).to(BF16)
+    assert np.array_equal(qt.double().numpy(), q)
+    s = sa.index_score_q8(qt[:, None].contiguous().to(dev), torch.ones((B, 1), device=dev), *C.pair(), i64(C.off, dev),
+                          i32([128] * B, dev), 128).double().cpu().numpy()
+    top = q[:, :1]
+    assert np.array_equal(s[q >= top * 2.0 ** -9], q[q >= top * 2.0 ** -9])
+    assert (np.abs(s - q) <= top * 2.0 ** -17).all()
