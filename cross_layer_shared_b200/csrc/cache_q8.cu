@@ -216,7 +216,9 @@ __global__ void __launch_bounds__(kThreadsC, kAppendCtas<F32, D, U>) cache_appen
 #pragma unroll
     for (int i = 0; i < kThreadsC / 32; ++i) mx = max(mx, warp_max[u][i]);
     const uint32_t bits = max(q8_scale_bits(mx), old_bits[u]);
-    const float inv = 1.f / __uint_as_float(bits);  // exact: a power of two
+    // exact for a power of two; a kept scale from elsewhere need not be one, and
+    // then this and the products below round once each, 2^-24 beside a code's 2^-4
+    const float inv = 1.f / __uint_as_float(bits);
     const int64_t row0 = first_row(h);
     uint8_t* dst = a.cache.codes[which] + row0 * D;
     const bool move = lo > 0 && bits != old_bits[u];  // the tokens already there go to the larger scale

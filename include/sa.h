@@ -616,8 +616,11 @@ sa_status sa_combine_partials(const float* O_part, int64_t o_stride, const float
  * n_b new tokens of sequence b go to places seq_len[b] - n_b .. seq_len[b]-1.
  * A block that already holds tokens keeps its scale unless the new ones
  * need a larger one; its older codes c then become the e4m3 values nearest
- * to c * old_scale / new_scale (exact, unless they become subnormal; an old
- * scale that is not positive and finite counts as 0).
+ * to c * old_scale / new_scale (exact, unless they become subnormal or the old
+ * scale is not a power of two; one that is not positive and finite counts as
+ * 0).  Under a kept scale that is not a power of two, x / scale is x times the
+ * scale's reciprocal, both rounded to fp32.  Elements from 248 * 2^120 on
+ * become 2^128, which reads back as infinity.
  * Places past seq_len[b] and all other blocks are left as they are.
  *   new_K, new_V  bf16 or fp32 (in_dtype) [n_rows, Hkv, d], one row of heads
  *             per token, stride_K / stride_V elements apart (so they may be

@@ -196,6 +196,46 @@ def test_calls_on_another_stream_with_memory_of_their_own(dev):
         assert all(torch.equal(a.cpu(), b.cpu()) for a, b in zip(want, got))
 
 
+# ------------------------------------------------------------------ appending behind scales from elsewhere
+@pytest.mark.parametrize("grow", [1.0, 300.0])
+@pytest.mark.parametrize("old", [0.7, 1.9999, 3e-3, 1e-39, 2.5e38])
+def test_append_behind_a_scale_that_is_not_a_power_of_two(old, grow, dev):
+    """The scale is kept where the new tokens fit, and x / scale is x times its reciprocal in fp32; else the older
+    codes move to the new scale."""
+    rng = np.random.default_rng(68)
+    old = np.float32(old)
+    C, Hkv, d, n0, n1 = Cache([64], 2, 128, dev), 2, 128, 20, 50
+    codes = rng.integers(0, 127, (Hkv, n0, d)).astype(np.uint8) | (rng.integers(0, 2, (Hkv, n0, d)) * 128).astype(np.uint8)
+    C.codes[0][:, :n0] = codes
+    C.scales[0][:] = old
+    C.upload()
+    with np.errstate(over="ignore"):
+        x = (rng.standard_normal((n1 - n0, Hkv, d)).astype(np.float32) * np.float32(min(60.0 * float(old) * grow, 3e37)))
+    ws = sa.workspace(sa.WS_HEADER_BYTES, dev)
+    sa.cache_append_q8(torch.from_numpy(x).to(dev), None, *C.pair(), None, None, i64(C.off, dev), i32([n1], dev),
+                       i64([0, n1 - n0], dev), ws=ws)
+    ok(ws)
+    for h in range(Hkv):
+        s = np.float32(max(q8.scale_of(float(np.abs(x[:, h]).max())), float(old)))
+        if s != old:
+            with np.errstate(under="ignore"):
+                ratio = old * (np.float32(1) / s)
+                C.codes[0][h, :n0] = q8.encode(q8.VALUES[codes[h]].astype(np.float32) * ratio)
+        C.codes[0][h, n0:n1] = q8.encode(x[:, h] * (np.float32(1) / s))
+        C.scales[0][h] = s
+    C.check()
+
+
+def test_the_largest_elements(dev):
+    """What rounds to 2^128 reads back as infinity, and what is just below does not."""
+    x = torch.tensor([3.4028234e38, -3.4028234e38, 3.29e38, -3.29e38] + [1.0] * 60).view(1, 1, 64)
+    C = Cache([64], 1, 64, dev, fill=0)
+    sa.cache_append_q8(x.to(dev), None, *C.pair(), None, None, i64(C.off, dev), i32([1], dev))
+    for dt in (F32, BF16):
+        got = sa.cache_read_q8(*C.pair(), None, None, i64(C.off, dev), i32([1], dev), 1, 1, idx=i32([[0]], dev), out_dtype=dt)
+        assert got[0, 0, 0, :4].double().tolist() == [np.inf, -np.inf, 240 * 2.0 ** 120, -240 * 2.0 ** 120]
+
+
 # ------------------------------------------------------------------ the queries' two parts
 def test_index_queries_keep_what_is_promised_of_them(dev):
     """One-hot keys give the query elements back: exact down to 2^-9 of their row's largest, and off by at most
