@@ -91,12 +91,16 @@ BINDING = os.path.join(PKG, "_binding.so")
 
 def build_binding(force: bool = False) -> str:
     """The marshalling of the 8-bit cache calls (csrc/binding.cpp): a Python
-    extension that reads torch's tensors; the entry points stay in libsa."""
+    extension that reads torch's tensors; the entry points stay in libsa.  It
+    needs g++ and the headers of Python and torch, and is built again for
+    another version of either."""
+    import torch
     src = os.path.join(CSRC, "binding.cpp")
-    if force or _stale(BINDING, [src, HEADER]):
+    stamp = os.path.join(BUILD, "binding.versions")
+    versions = f"python {sys.version}\ntorch {torch.__version__} {torch.version.git_version}\n"
+    if force or _stale(BINDING, [src, HEADER]) or _read(stamp) != versions:
         import sysconfig
 
-        import torch
         base = os.path.dirname(torch.__file__)
         cuda = os.path.dirname(os.path.dirname(nvcc()))
         inc = [sysconfig.get_paths()["include"], os.path.join(base, "include"),
@@ -105,21 +109,35 @@ def build_binding(force: bool = False) -> str:
         cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{i}" for i in inc), src, "-o",
                BINDING + ".tmp", f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
-        r = subprocess.run(cmd, capture_output=True, text=True)
+        try:
+            r = subprocess.run(cmd, capture_output=True, text=True)
+        except FileNotFoundError as e:
+            raise RuntimeError("binding.cpp needs g++ (libsa itself is built)") from e
         if r.returncode != 0:
-            raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"g++ failed on binding.cpp (libsa itself is built):\n{r.stdout}\n{r.stderr}")
         os.replace(BINDING + ".tmp", BINDING)
+        os.makedirs(BUILD, exist_ok=True)
+        with open(stamp, "w") as f:
+            f.write(versions)
     return BINDING
+
+
+def _read(path: str) -> str:
+    try:
+        with open(path) as f:
+            return f.read()
+    except FileNotFoundError:
+        return ""
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     _build_lib(LIB, BUILD, (), force)
-    build_binding(force)
     if force or _stale(SYNTH_LIB, [SYNTH_SRC]):
         cmd = [nvcc(), *NVFLAGS, "-shared", "-o", SYNTH_LIB + ".tmp", SYNTH_SRC]
         subprocess.check_call(cmd)
         os.replace(SYNTH_LIB + ".tmp", SYNTH_LIB)
+    build_binding(force)  # last: it alone needs more than nvcc
     if verbose:
         print("built", LIB, "and", SYNTH_LIB)
     return LIB

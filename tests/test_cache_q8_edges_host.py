@@ -3,11 +3,13 @@ and refusals of the C entry points, and what the Python calls do around them."""
 import ast
 import ctypes
 import inspect
+import subprocess
 
 import pytest
 import torch
 
 import cross_layer_shared_b200 as sa
+from cross_layer_shared_b200 import build
 from tests.test_cache_q8_host import append, attn, lib  # noqa: F401
 
 
@@ -115,3 +117,46 @@ def test_room_to_grow_does_not_change_the_plan(lib, B, Hq, Hkv, S_max):
     size = sa.decode_attn_q8_workspace_size
     tight = B * (S_max + 63) // 64 * 64
     assert size(1, B, 1 << 20, S_max, Hq, Hkv, 128, 0) == size(1, B, tight, S_max, Hq, Hkv, 128, 0)
+
+
+# ------------------------------------------------------------------ the build of the marshalling
+def test_binding_is_built_again_for_another_torch(monkeypatch, tmp_path):
+    built = []
+
+    def gxx(cmd, **kw):
+        built.append(cmd[0])
+        (tmp_path / "_binding.so.tmp").write_text("")
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(build, "BINDING", str(tmp_path / "_binding.so"))
+    monkeypatch.setattr(build, "BUILD", str(tmp_path))
+    monkeypatch.setattr(build.subprocess, "run", gxx)
+    build.build_binding()
+    build.build_binding()
+    assert built == ["g++"]
+    monkeypatch.setattr(torch, "__version__", "0.0.0")
+    build.build_binding()
+    build.build_binding()
+    assert built == ["g++"] * 2
+
+
+def test_libraries_are_built_without_what_the_binding_needs(monkeypatch, tmp_path):
+    """A host without g++ or headers still gets libsa and the generator, then the error."""
+    done = []
+    monkeypatch.setattr(build, "BUILD", str(tmp_path))
+    monkeypatch.setattr(build, "SYNTH_LIB", str(tmp_path / "libsasynth.so"))
+    monkeypatch.setattr(build, "_build_lib", lambda out, *a: done.append(out))
+
+    def check_call(cmd):
+        done.append(cmd[-1])
+        (tmp_path / "libsasynth.so.tmp").write_text("")
+
+    def missing(*a, **kw):
+        raise FileNotFoundError("g++")
+
+    monkeypatch.setattr(build.subprocess, "check_call", check_call)
+    monkeypatch.setattr(build.subprocess, "run", missing)
+    monkeypatch.setattr(build, "BINDING", str(tmp_path / "_binding.so"))
+    with pytest.raises(RuntimeError, match="g\\+\\+"):
+        build.build()
+    assert done == [build.LIB, build.SYNTH_SRC]
