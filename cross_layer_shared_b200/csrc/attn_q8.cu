@@ -130,14 +130,14 @@ __device__ __forceinline__ void cp_async4(void* dst, const void* src, uint32_t s
                : "memory");
 }
 
-// a scale >= 0 as f 2^e, 1 <= f < 2.  Zero has f = 0 and an exponent below
-// every other one's, so that a key without a contribution does not set the
-// reference of those that have one.
+// a scale >= 0 as f 2^e: 1 <= f < 2, or from zero up to 2^-126 f < 1 and e =
+// -126, so that a key without a contribution does not set the reference of
+// those that have one (beside it 2^-32 of 448 2^-126 may be lost: nothing)
 __device__ __forceinline__ void split_scale(float s, float& f, float& e) {
-  const bool tiny = s < 0x1p-126f;  // zero or subnormal: normalised first
-  const uint32_t u = __float_as_uint(tiny ? s * 0x1p24f : s);
-  f = s == 0.f ? 0.f : __uint_as_float((u & 0x7fffffu) | 0x3f800000u);
-  e = (float)((int)(u >> 23 & 0xff) - (tiny ? 127 + 24 : 127));
+  const uint32_t u = __float_as_uint(s);
+  const int x = (int)(u >> 23 & 0xff);
+  f = x == 0 ? s * 0x1p126f : __uint_as_float((u & 0x7fffffu) | 0x3f800000u);
+  e = (float)(max(x, 1) - 127);
 }
 
 // max over the 8 lanes that hold one query row's keys
