@@ -51,7 +51,7 @@
 //
 // Measured (B200, warm graph replay): every token of 4 x 131072, 32 query and 8
 // KV heads, 178 us = 92 % of the measured HBM rate; 8 sequences over 2048
-// picked tokens, 32 / 4 heads, 10.1 us (17 MB: latency); two sequences of 333
+// picked tokens, 32 / 4 heads, 10.2 us (17 MB: latency); two sequences of 333
 // and 1021 tokens 5.5 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

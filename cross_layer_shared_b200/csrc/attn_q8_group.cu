@@ -6,7 +6,8 @@
 // 512 R flops.  From about 16 rows the warp-level MMAs of attn_q8.cu, whose
 // warps each convert all codes they multiply, are issue-bound; here each code
 // is converted once per 128 rows and the products run on tcgen05 (S and O in
-// TMEM), so what is left is latency: a slice of an index is a handful of tiles.
+// TMEM).  What is left is latency around a slice's handful of tiles, and for
+// each tile the conversion.
 //
 //   * Warps 9-16 (producers) load the codes of a tile straight into registers
 //     (16 bytes a lane, the next K and V pieces in flight while the last ones

@@ -20,7 +20,7 @@
 // by a scan over the sequences, 32 at a time.
 //
 // Measured (B200, warm graph replay): those 16 prompts, fp32, 4 heads of 128, K
-// and V, 122 us = 86 % of the measured HBM rate; 2048 bf16 tokens of 8 heads
+// and V, 124 us = 85 % of the measured HBM rate; 2048 bf16 tokens of 8 heads
 // 6.1 us; one token of 4 sequences 2.4 us.  Reading 131009 tokens of 8 heads
 // back as bf16 takes 121.7 us = the measured HBM rate.
 #include <cuda_fp16.h>
