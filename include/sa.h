@@ -687,7 +687,8 @@ sa_status sa_index_score_q8(const void* qI, const float* w, const void* KI8, con
  * Device errors: idx entry >= seq_len[b] -> SA_ERR_DEVICE, entry skipped.
  * Keys are split over several CTAs.  Where those are more than a cluster,
  * their partial results meet in the workspace (some counted in its header),
- * whose size this gives: */
+ * whose size this gives, for exactly these arguments (fewer sequences or a
+ * smaller S_max may be split further and need more): */
 size_t sa_decode_attn_q8_workspace_size(int L_g, int B, int64_t n_tokens, int S_max, int Hq, int Hkv, int d, int k);
 sa_status sa_decode_attn_q8(const void* Q, const void* K8, const float* K_scale, const void* V8,
                             const float* V_scale, const int64_t* seq_off, const int32_t* seq_len,
